@@ -1,4 +1,5 @@
-"""MI355X-native error-feedback Top-k gradient compression.
+"""MI355X-native error-feedback Top-k gradient compression, and 8-bit activation checkpoints with
+the weight gradients formed from them.
 
 A thin Python binding over the C ABI of ``libgc.so`` (``include/gc.h``): argument
 marshalling only, every step of the path runs in the library's HIP kernels.  PyTorch is used
@@ -38,7 +39,10 @@ EXPORTS = ("gc_plan_create", "gc_plan_destroy", "gc_plan_total_k", "gc_plan_layo
            "gc_status_string", "gc_sign_ef_compress", "gc_plan_sign_layout",
            "gc_sign_decompress", "gc_qsgd_compress", "gc_qsgd_decompress",
            "gc_threshold_ef_compress", "gc_randk_compress", "gc_decompress_gathered",
-           "gc_clip_by_norm", "gc_clip_factors", "gc_plan_set_gradient_scale", "gc_layout")
+           "gc_clip_by_norm", "gc_clip_factors", "gc_plan_set_gradient_scale", "gc_layout",
+           "gc_act_layout", "gc_act_quant", "gc_act_restore", "gc_rmsnorm",
+           "gc_rmsnorm_backward_workspace", "gc_rmsnorm_backward",
+           "gc_act_weight_grad_workspace", "gc_act_weight_grad")
 
 _libs: dict = {}
 
@@ -98,6 +102,17 @@ def lib(variant: str | None = None) -> ctypes.CDLL:
         "gc_clip_factors": [vp, vp, vp, vp, vp, vp],
         "gc_plan_set_gradient_scale": [vp, vp],
         "gc_layout": [vp, i32, vp, vp, vp, vp],
+        "gc_act_layout": [i64, vp, vp],
+        "gc_act_quant": [vp, i64, i32, i64, i64, i32, u64, u64, vp, vp, vp],
+        "gc_act_restore": [vp, vp, i64, i64, vp, i64, i32, vp],
+        "gc_rmsnorm": [vp, i64, vp, i64, i32, i64, i64, vp, i32, f32, vp, i64, vp, i64, vp, vp,
+                       vp, i32, u64, u64, vp],
+        "gc_rmsnorm_backward_workspace": [i64, i64, vp],
+        "gc_rmsnorm_backward": [vp, i64, i32, i64, i64, vp, vp, vp, vp, i32, vp, i64, vp, i64, vp,
+                                ctypes.c_int, vp, i64, vp],
+        "gc_act_weight_grad_workspace": [i64, i64, i64, i32, vp],
+        "gc_act_weight_grad": [vp, i64, i32, i64, i64, i64, vp, vp, vp, i32, vp, ctypes.c_int, vp,
+                               i64, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -474,7 +489,235 @@ def read_f32(x, sink, stream=None):
            "gc_read_f32")
 
 
+# ------------------------------------------------------------ activation checkpoints (8 bits)
+ACT_GROUP = 32        # columns that share a scale
+_GC_DTYPES = {"float32": 0, "bfloat16": 1, "float16": 2}
+
+
+def act_layout(cols: int):
+    """(pitch, groups) of a checkpoint's rows: codes are int8[rows, pitch], exps uint8[rows,
+    groups] (host-only)."""
+    pitch, groups = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().gc_act_layout(int(cols), ctypes.byref(pitch), ctypes.byref(groups)),
+           "gc_act_layout")
+    return pitch.value, groups.value
+
+
+def _dtype_code(t, name):
+    if t is None:
+        raise TypeError(f"{name} must be a torch tensor")
+    code = _GC_DTYPES.get(str(t.dtype).rpartition(".")[2])
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _on_device(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on the GPU")
+    cur = torch.cuda.current_device()
+    if t.device.index != cur:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def _matrix(t, name, like=None, like_name=""):
+    """(pointer, row pitch, rows, columns) of a tensor whose last dimension is the columns (unit
+    stride) and whose other dimensions are evenly spaced rows; with ``like``, of its shape and
+    type.  None -> a NULL matrix."""
+    if t is None:
+        return None, 0, 0, 0
+    _on_device(t, name)
+    if t.dim() < 1:
+        raise ValueError(f"{name} needs a dimension of columns")
+    cols = t.shape[-1]
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    if cols == 0 or rows == 0:
+        m = (None, 0, rows, cols)
+    else:
+        if cols > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have unit stride along its last dimension")
+        lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+        for (_, outer), (n, inner) in zip(lead, lead[1:]):
+            if outer != n * inner:
+                raise ValueError(f"{name} must have evenly spaced rows")
+        ld = lead[-1][1] if lead else cols
+        if ld < cols:
+            raise ValueError(f"{name} has overlapping rows")
+        m = (ctypes.c_void_p(t.data_ptr()), ld, rows, cols)
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
+        if tuple(t.shape) != tuple(like.shape):
+            raise ValueError(f"{name} must have the shape of {like_name}, {tuple(like.shape)}, "
+                             f"got {tuple(t.shape)}")
+    return m
+
+
+def _checkpoint(codes, exps, rows, cols):
+    """Device pointers of the two arrays of a rows x cols checkpoint."""
+    import torch
+    pitch, groups = act_layout(cols)
+    out = []
+    for t, dtype, name, width in ((codes, torch.int8, "codes", pitch),
+                                  (exps, torch.uint8, "exps", groups)):
+        out.append(_dev_ptr(t, dtype, name))
+        if t is not None and t.numel() != rows * width:
+            raise ValueError(f"{name} must hold {rows} x {width} elements, has {t.numel()}")
+    return out
+
+
+def _vector(t, name, cols):
+    """(pointer, type code) of a vector over the columns; NULL for None."""
+    if t is None:
+        return None, 0
+    code = _dtype_code(t, name)
+    p = _dev_ptr(t, t.dtype, name)
+    if t.numel() != cols:
+        raise ValueError(f"{name} must have {cols} elements, has {t.numel()}")
+    return p, code
+
+
+def _rounding(stochastic, seed, step):
+    return int(bool(stochastic)), int(seed) & (2 ** 64 - 1), int(step) & (2 ** 64 - 1)
+
+
+def _workspace(workspace, need, stream):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one on the stream."""
+    import torch
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+    p = _dev_ptr(workspace, workspace.dtype, "workspace")
+    return p, workspace.numel() * workspace.element_size(), workspace
+
+
+def act_quant(x, codes, exps, stochastic: bool = False, seed: int = 0, step: int = 0,
+              stream=None):
+    """x into its 8-bit checkpoint: one power-of-two scale for 32 columns of a row, codes rounded
+    to nearest even or, with ``stochastic``, by the Philox stream of (seed, step)."""
+    p, ld, rows, cols = _matrix(x, "x")
+    code = _dtype_code(x, "x")
+    cp, ep = _checkpoint(codes, exps, rows, cols)
+    _check(lib().gc_act_quant(p, ld, code, rows, cols, *_rounding(stochastic, seed, step), cp, ep,
+                              _stream(stream)), "gc_act_quant")
+
+
+def act_restore(codes, exps, out, stream=None):
+    """out = the checkpoint's values, rounded to out's type (exact in float32 and bfloat16)."""
+    p, ld, rows, cols = _matrix(out, "out")
+    code = _dtype_code(out, "out")
+    cp, ep = _checkpoint(codes, exps, rows, cols)
+    _check(lib().gc_act_restore(cp, ep, rows, cols, p, ld, code, _stream(stream)),
+           "gc_act_restore")
+
+
+def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, h=None, y=None, rstd=None,
+            codes=None, exps=None, stochastic: bool = False, seed: int = 0, step: int = 0,
+            stream=None):
+    """h = x + residual; rstd = 1 / sqrt(mean(h^2) + eps); z = h * rstd; y = z * weight, and z's
+    8-bit checkpoint into (codes, exps).  ``h``, ``y``, ``rstd`` (float32[rows]) and the
+    checkpoint are written where given (at least y or the checkpoint); h or y may be x or
+    residual itself."""
+    import torch
+    xp, ld_x, rows, cols = _matrix(x, "x")
+    code = _dtype_code(x, "x")
+    rp, ld_r, _, _ = _matrix(residual, "residual", x, "x")
+    hp, ld_h, _, _ = _matrix(h, "h", x, "x")
+    yp, ld_y, _, _ = _matrix(y, "y", x, "x")
+    wp, wcode = _vector(weight, "weight", cols)
+    cp = ep = None
+    if codes is not None or exps is not None:
+        if codes is None or exps is None:
+            raise ValueError("codes and exps go together")
+        cp, ep = _checkpoint(codes, exps, rows, cols)
+    _check(lib().gc_rmsnorm(xp, ld_x, rp, ld_r, code, rows, cols, wp, wcode, float(eps), hp, ld_h,
+                            yp, ld_y, _dev_ptr(rstd, torch.float32, "rstd", rows), cp, ep,
+                            *_rounding(stochastic, seed, step), _stream(stream)), "gc_rmsnorm")
+
+
+def rmsnorm_backward_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace of a rmsnorm_backward call with dweight (host-only)."""
+    n = ctypes.c_int64()
+    _check(lib().gc_rmsnorm_backward_workspace(int(rows), int(cols), ctypes.byref(n)),
+           "gc_rmsnorm_backward_workspace")
+    return n.value
+
+
+def rmsnorm_backward(dy, codes, exps, rstd, dx, weight=None, dres=None, dweight=None,
+                     accumulate: bool = False, workspace=None, stream=None):
+    """The norm's backward pass from its checkpoint: dx = rstd * (t - z * mean(t * z)) + dres with
+    t = dy * weight; dweight (float32, a segment of the flat gradient) = sum over rows of dy * z,
+    added to what it holds with ``accumulate``.  dx may be dy or dres itself.  ``workspace``: a
+    tensor of rmsnorm_backward_workspace bytes; allocated for the call when None."""
+    import torch
+    p, ld, rows, cols = _matrix(dy, "dy")
+    code = _dtype_code(dy, "dy")
+    xp, ld_x, _, _ = _matrix(dx, "dx", dy, "dy")
+    if dx is None:
+        raise TypeError("dx must be a torch tensor")
+    rp, ld_r, _, _ = _matrix(dres, "dres", dy, "dy")
+    cp, ep = _checkpoint(codes, exps, rows, cols)
+    wp, wcode = _vector(weight, "weight", cols)
+    dwp = _dev_ptr(dweight, torch.float32, "dweight")
+    need = 0
+    if dweight is not None:
+        if dweight.numel() != cols:
+            raise ValueError(f"dweight must have {cols} elements, has {dweight.numel()}")
+        need = rmsnorm_backward_workspace(rows, cols)
+    ws, ws_bytes, _keep = _workspace(workspace, need, stream)
+    _check(lib().gc_rmsnorm_backward(p, ld, code, rows, cols, cp, ep,
+                                     _dev_ptr(rstd, torch.float32, "rstd", rows), wp, wcode, rp,
+                                     ld_r, xp, ld_x, dwp, int(bool(accumulate)), ws, ws_bytes,
+                                     _stream(stream)), "gc_rmsnorm_backward")
+
+
+def act_weight_grad_workspace(rows: int, n_out: int, cols: int, dtype) -> int:
+    """Bytes of workspace of an act_weight_grad call (host-only); ``dtype``: dy's."""
+    code = _GC_DTYPES.get(str(dtype).rpartition(".")[2], -1)
+    n = ctypes.c_int64()
+    _check(lib().gc_act_weight_grad_workspace(int(rows), int(n_out), int(cols), code,
+                                              ctypes.byref(n)), "gc_act_weight_grad_workspace")
+    return n.value
+
+
+def act_weight_grad(dy, codes, exps, dweight, col_scale=None, accumulate: bool = False,
+                    workspace=None, stream=None):
+    """dweight[n, k] = col_scale[k] * sum over rows of dy[:, n] * z[:, k], z the checkpoint's
+    values: a linear layer's weight gradient from its kept input.  ``dweight`` (float32[n_out,
+    cols], a segment of the flat gradient viewed so) is added to with ``accumulate``.
+    ``workspace``: a tensor of act_weight_grad_workspace bytes; allocated for the call when
+    None."""
+    import torch
+    p, ld, rows, n_out = _matrix(dy, "dy")
+    code = _dtype_code(dy, "dy")
+    dwp = _dev_ptr(dweight, torch.float32, "dweight")
+    if dweight is None:
+        raise TypeError("dweight must be a torch tensor")
+    if dweight.dim() != 2 or dweight.shape[0] != n_out:
+        raise ValueError(f"dweight must be {n_out} x columns, got {tuple(dweight.shape)}")
+    cols = dweight.shape[1]
+    cp, ep = _checkpoint(codes, exps, rows, cols)
+    sp, scode = _vector(col_scale, "col_scale", cols)
+    need = act_weight_grad_workspace(rows, n_out, cols, dy.dtype)
+    ws, ws_bytes, _keep = _workspace(workspace, need, stream)
+    _check(lib().gc_act_weight_grad(p, ld, code, rows, n_out, cols, cp, ep, sp, scode, dwp,
+                                    int(bool(accumulate)), ws, ws_bytes, _stream(stream)),
+           "gc_act_weight_grad")
+
+
 __all__ = ["Plan", "GCError", "lib", "status_string", "copy_f32", "add_f32", "read_f32", "layout",
-           "topk_ef_compress_noalloc", "EXPORTS",
+           "topk_ef_compress_noalloc", "EXPORTS", "act_layout", "act_quant", "act_restore",
+           "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace", "act_weight_grad",
+           "act_weight_grad_workspace", "ACT_GROUP",
            "GC_MOMENTUM_MASK", "GC_DEBUG_FORCE_FALLBACK", "GC_DEBUG_NO_ESTIMATE", "GC_DEBUG_CHAIN", "MODE_SKIP",
            "MODE_CANDIDATES", "MODE_FULL", "MODE_RECAPTURED", "MODE_SMALL", "SMALL_SEGMENT"]

@@ -13,12 +13,19 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libgc.so")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("gc_pass.hip", "gc_topk.hip", "gc_codecs.hip",
-                                                       "gc_scatter.hip", "gc_api.hip")]
+# The compressors, whose kernels follow the tile geometry, and the activation operators, whose
+# kernels do not (every library holds both).
+TILED = [os.path.join(HERE, "csrc", f) for f in ("gc_pass.hip", "gc_topk.hip", "gc_codecs.hip",
+                                                     "gc_scatter.hip", "gc_api.hip")]
+ACTIVATION = [os.path.join(HERE, "csrc", f) for f in ("gc_act.hip", "gc_norm.hip",
+                                                          "gc_wgrad.hip", "gc_act_api.hip")]
+SOURCES = TILED + ACTIVATION
 ARCH = "gfx950"
 
 # Tile geometries besides the default (1024 threads x 2 slots, 8192-element tiles).  A tile is
@@ -53,11 +60,7 @@ def flags() -> list[str]:
             "-I", os.path.join(HERE, "csrc")]
 
 
-def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
-    """Compile libgc.so; ``defines`` (e.g. "GC_TILE_SLOTS=4") override the compile-time
-    configuration of the streaming pass."""
-    tmp = out + f".tmp{os.getpid()}"
-    cmd = [hipcc(), *flags(), *[f"-D{d}" for d in defines], *SOURCES, "-o", tmp]
+def _run(cmd, verbose: bool):
     res = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     err = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if noise not in l)
@@ -65,17 +68,43 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err)
-    os.replace(tmp, out)
-    return out
+
+
+def _build(jobs, verbose: bool) -> list[str]:
+    """Compile each library's sources side by side, then link it; ``jobs`` lists (output,
+    defines).  The activation sources are compiled once for all of them."""
+    compile_flags = [f for f in flags() if f != "-shared"]
+    with tempfile.TemporaryDirectory() as tmp, \
+            ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
+        def compiled(src, tag, defines):
+            obj = os.path.join(tmp, f"{os.path.basename(src)}.{tag}.o")
+            cmd = [hipcc(), *compile_flags, *[f"-D{d}" for d in defines], "-c", src, "-o", obj]
+            return obj, ex.submit(_run, cmd, verbose)
+
+        tiled = [[compiled(src, i, defines) for src in TILED]
+                 for i, (_, defines) in enumerate(jobs)]
+        shared = [compiled(src, "act", ()) for src in ACTIVATION]
+
+        def link(out, objs):
+            for _, fut in objs:
+                fut.result()
+            new = out + f".tmp{os.getpid()}"
+            _run([hipcc(), *flags(), *[o for o, _ in objs], "-o", new], verbose)
+            os.replace(new, out)
+            return out
+
+        return [link(out, objs + shared) for (out, _), objs in zip(jobs, tiled)]
+
+
+def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
+    """Compile libgc.so; ``defines`` (e.g. "GC_TILE_SLOTS=4") override the compile-time
+    configuration of the streaming pass."""
+    return _build([(out, defines)], verbose)[0]
 
 
 def build_all(verbose: bool = False) -> list[str]:
-    """libgc.so and every VARIANTS geometry (the hipcc runs in parallel)."""
-    from concurrent.futures import ThreadPoolExecutor
-    jobs = [(LIB, ())] + [(variant_path(n), d) for n, d in VARIANTS.items()]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-        futs = [ex.submit(build, verbose, out, d) for out, d in jobs]
-        return [f.result() for f in futs]
+    """libgc.so and every VARIANTS geometry."""
+    return _build([(LIB, ())] + [(variant_path(n), d) for n, d in VARIANTS.items()], verbose)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,189 @@
+// gc_act.h -- device-side building blocks of the activation operators: the element types, the
+// 8-bit checkpoint format (groups of 32 columns, a power-of-two scale each) and the lane layout
+// that its writers share.
+//
+// An octet is 8 consecutive columns of a row, held by one lane: one 16-byte load of a 16-bit
+// type, 8 bytes of codes.  A group is the 4 octets of 4 neighbouring lanes, so its largest
+// magnitude is two steps inside the quad.
+#pragma once
+
+#include "gc_random.h"
+
+namespace gc {
+namespace {
+
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+constexpr int kActGroup = 32;          // columns that share a scale
+constexpr uint32_t kExpLowest = 7;     // 2^-120: every restored value is a normal number (or 0)
+constexpr uint32_t kExpHighest = 248;  // 2^121: 127 * 2^121 is finite
+constexpr uint32_t kExpBad = 255;      // 2^128 = Inf, with codes 0: the group restores to NaN
+constexpr uint32_t kActTag = 0x54u;    // Philox counter tag of the stochastic rounding
+
+template <int DT>
+struct Elt;
+template <>
+struct Elt<kF32> {
+  typedef float T;
+};
+template <>
+struct Elt<kBF16> {
+  typedef __bf16 T;
+};
+template <>
+struct Elt<kF16> {
+  typedef _Float16 T;
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(_Float16 x) { return (float)x; }
+// bf16 is the upper half of the binary32 bits
+__device__ __forceinline__ float to_float(__bf16 x) {
+  return __uint_as_float((uint32_t)__builtin_bit_cast(uint16_t, x) << 16);
+}
+
+// One value of a vector over the columns whose type is only known at run time.
+__device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
+  return dtype == kF32    ? static_cast<const float*>(p)[i]
+         : dtype == kBF16 ? to_float(static_cast<const __bf16*>(p)[i])
+                          : (float)static_cast<const _Float16*>(p)[i];
+}
+
+// 8 columns from col of the row at p.  kVec: p and the row pitch are multiples of 16 bytes, so
+// a whole octet is loaded in 16-byte pieces.  Columns from `cols` on give 0.
+template <int DT, bool kVec>
+__device__ __forceinline__ void load8(const typename Elt<DT>::T* p, int col, int cols,
+                                      float (&v)[8]) {
+  typedef typename Elt<DT>::T T;
+  if (kVec && col + 8 <= cols) {
+    T raw[8];
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<u4*>(raw) = *reinterpret_cast<const u4*>(p + col);
+    } else {
+      reinterpret_cast<u4*>(raw)[0] = reinterpret_cast<const u4*>(p + col)[0];
+      reinterpret_cast<u4*>(raw)[1] = reinterpret_cast<const u4*>(p + col)[1];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = to_float(raw[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = col + j < cols ? to_float(p[col + j]) : 0.0f;
+  }
+}
+
+// A fp32 value rounded to the type, nearest even.  For fp16 the value is made opaque first: the
+// compiler otherwise joins a product and its conversion into one instruction that rounds once,
+// and the stored value would not be the rounded fp32 product.
+template <int DT>
+__device__ __forceinline__ typename Elt<DT>::T round_to(float x) {
+  if (DT == kF16) asm("" : "+v"(x));
+  return (typename Elt<DT>::T)x;
+}
+
+// Rounds v to the type and stores the columns below `cols`.
+template <int DT, bool kVec>
+__device__ __forceinline__ void store8(typename Elt<DT>::T* p, int col, int cols,
+                                       const float (&v)[8]) {
+  typedef typename Elt<DT>::T T;
+  if (kVec && col + 8 <= cols) {
+    T raw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) raw[j] = round_to<DT>(v[j]);
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<u4*>(p + col) = *reinterpret_cast<u4*>(raw);
+    } else {
+      reinterpret_cast<u4*>(p + col)[0] = reinterpret_cast<u4*>(raw)[0];
+      reinterpret_cast<u4*>(p + col)[1] = reinterpret_cast<u4*>(raw)[1];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < cols) p[col + j] = round_to<DT>(v[j]);
+  }
+}
+
+// Largest of a value over the lane's quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));   // lanes 1,0,3,2
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));  // 2,3,0,1
+}
+
+// Biased exponent of the group's scale from its largest magnitude's bits: the smallest
+// e >= -120 with A <= 127 * 2^e.  With A = f * 2^p and f in [1, 2), e = p - 6 where
+// f <= 127/64 (mantissa bits <= 0x7E0000) and p - 5 above it: adding 0x1FFFF carries into the
+// exponent just there.  Inf, NaN and anything above 127 * 2^121 give kExpBad.
+__device__ __forceinline__ uint32_t group_exponent(uint32_t amax) {
+  const uint32_t e = ((amax + 0x1FFFFu) >> 23);
+  return e < kExpLowest + 6 ? kExpLowest : e > kExpHighest + 6 ? kExpBad : e - 6;
+}
+
+__device__ __forceinline__ float exponent_scale(uint32_t e) { return __uint_as_float(e << 23); }
+
+// The octet's codes (column order = byte order) and its group's exponent.  Every lane of the
+// quad calls it.  x * 2^-e is exact, so the code of a value is the same however it was formed:
+// rounded to nearest even by adding 1.5 * 2^23, whose unit is 1; or, with kRandom, floor or
+// ceiling of the magnitude by the 24-bit draws of blocks `block` and `block + 1` (4 columns each).
+template <bool kRandom>
+__device__ __forceinline__ u2 encode8(const float (&v)[8], uint64_t block, uint32_t seed_lo,
+                                      uint32_t seed_hi, uint32_t step_lo, uint32_t* exponent) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = max(amax, mag_key(v[j]));
+  const uint32_t e = group_exponent(quad_max(amax));
+  *exponent = e;
+  uint32_t q[8];
+  if (kRandom) {
+    uint32_t w[8];
+    uint32_t w0[4], w1[4];
+    philox4((uint32_t)block, (uint32_t)(block >> 32), step_lo, kActTag, seed_lo, seed_hi, w0);
+    ++block;
+    philox4((uint32_t)block, (uint32_t)(block >> 32), step_lo, kActTag, seed_lo, seed_hi, w1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = w0[j] >> 8;
+      w[4 + j] = w1[j] >> 8;
+    }
+    const float inv = __uint_as_float((254u - min(e, kExpHighest)) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(v[j]) * inv, f = floorf(a);
+      const int m = (int)f + ((float)w[j] < (a - f) * 16777216.0f ? 1 : 0);
+      q[j] = (uint32_t)(signbit(v[j]) ? -m : m);
+    }
+  } else {
+    const float inv = __uint_as_float((254u - min(e, kExpHighest)) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(v[j] * inv + 12582912.0f);
+  }
+  u2 r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t* p = q + 4 * h;
+    const uint32_t lo = __builtin_amdgcn_perm(p[1], p[0], 0x0C0C0400);
+    const uint32_t hi = __builtin_amdgcn_perm(p[3], p[2], 0x0C0C0400);
+    r[h] = lo | (hi << 16);
+  }
+  return e == kExpBad ? u2{0, 0} : r;
+}
+
+// code * scale for 8 codes: exact (7 bits and a sign times a power of two); 0 * Inf is the NaN
+// of a bad group.
+__device__ __forceinline__ void decode8(u2 c, float scale, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[4 * h + j] = (float)(int8_t)(c[h] >> (8 * j)) * scale;
+}
+
+// How the writers and readers of whole rows spread octets over waves: a row has `octets`
+// octets; rows of fewer than 64 share a wave (64 / lanes rows of `lanes` lanes, a power of two of
+// at least 4), longer ones take `chunks` wave units of 64 octets each.
+struct RowMap {
+  int64_t rows, units;   // wave units in all
+  int32_t cols, octets, chunks, lanes;
+};
+
+}  // namespace
+}  // namespace gc

@@ -373,6 +373,113 @@ int gc_decompress_gathered(const gc_plan* plan, int32_t n_workers, const float* 
                            const int8_t* codes, const float* scales, const int32_t* idx,
                            float* dense, int accumulate, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits, and the gradients formed from them.
+ *
+ * What stands between a training step's activations and the flat gradient that the calls above
+ * compress: the input of a linear layer is kept for the backward pass in 8 bits instead of 16 or
+ * 32, by itself (gc_act_quant) or by the norm in front of it (gc_rmsnorm), and the backward pass
+ * reads the kept form (gc_act_weight_grad, gc_rmsnorm_backward, or gc_act_restore for any other
+ * use).  The weight gradients are fp32 and go straight into their segments of the flat gradient.
+ *
+ * The checkpoint of a rows x cols matrix: 32 consecutive columns of a row are a group (the last
+ * one may be short), pitch = 32 * ceil(cols / 32), groups = pitch / 32 (gc_act_layout).
+ *   codes : int8[rows][pitch], 16-byte aligned; columns from cols on hold 0.
+ *   exps  : uint8[rows][groups], the biased exponent b of each group's scale 2^(b - 127).
+ * Definition, per group with A = the largest |x|:
+ *   e = the smallest integer >= -120 with A <= 127 * 2^e;  b = e + 127;  a = |x| / 2^e (exact)
+ *   GC_ROUND_NEAREST    : code = x / 2^e rounded to the nearest integer, ties to even;
+ *   GC_ROUND_STOCHASTIC : code = sign(x) * (floor(a) + [u24 < (a - floor(a)) * 2^24]), u24 the top
+ *         24 bits of word (i % 4) of the Philox4x32-10 block keyed (seed low 32 bits, seed high 32
+ *         bits) at counter (i / 4 low, i / 4 high, step low 32, 0x54), i = row * pitch + column:
+ *         the restored value's expectation is x;
+ *   a group that holds Inf or NaN, or A > 127 * 2^121: b = 255 and codes 0.
+ * Restored value: code * 2^(b - 127), exact in fp32 and in bf16 (a group of b = 255 is NaN).  The
+ * error is at most 2^(e-1) (nearest), below 2^e (stochastic); 2^e < A / 63.
+ *
+ * Matrices are row-major with unit column stride and a row pitch `ld` in elements (ld >= cols),
+ * of a gc_dtype.  No alignment beyond the element's is required of them; 16-byte aligned rows
+ * (pointer and pitch) are faster.  Rows or columns of 0 are allowed.  Sums are in fp32 (the norm's
+ * square sum in double) in an order that depends on the sizes alone, so that repeated calls give
+ * the same bits.  These calls keep nothing between calls; a workspace belongs to one call at a
+ * time.  An output may be the very same matrix (pointer and pitch) as an input where stated; any
+ * other shared byte between an output and another buffer is an error.
+ * Limits (GC_ERR_UNSUPPORTED beyond them): rows <= 2^25, rows * pitch <= 2^34, cols and n_out
+ * < 2^31, n_out * cols < 2^31, cols <= 32768 for the norm.
+ * Errors: GC_ERR_INVALID_ARG (nothing launched), GC_ERR_UNSUPPORTED, GC_ERR_HIP.
+ */
+typedef enum { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 } gc_dtype;
+#define GC_ROUND_NEAREST 0
+#define GC_ROUND_STOCHASTIC 1
+
+/* Host-only: the pitch and the groups of a row of `cols` columns (either may be NULL). */
+int gc_act_layout(int64_t cols, int64_t* pitch /* host */, int64_t* groups /* host */);
+
+/* x (rows x cols) into its checkpoint.  rounding: GC_ROUND_NEAREST (seed and step are ignored) or
+ * GC_ROUND_STOCHASTIC. */
+int gc_act_quant(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t cols,
+                 int32_t rounding, uint64_t seed, uint64_t step, int8_t* codes, uint8_t* exps,
+                 void* stream);
+
+/* out = the restored values, rounded to dtype (nearest even; exact in fp32 and bf16). */
+int gc_act_restore(const int8_t* codes, const uint8_t* exps, int64_t rows, int64_t cols,
+                   void* out, int64_t ld_out, int32_t dtype, void* stream);
+
+/*
+ * Root-mean-square norm of x, after the addition of the residual stream, per row:
+ *   h = round(x + residual) to dtype (h = x without a residual);
+ *   rstd = fl32(1 / sqrt(S / cols + eps)), S = sum h^2 in double (order unspecified);
+ *   z = fl32(h * rstd);   y = round(fl32(z * weight)) to dtype (weight 1 where NULL);
+ *   the checkpoint holds z, the normalised row before its weight.
+ * The backward pass needs z itself; a layer behind the norm multiplies by the weight in its
+ * weight gradient's columns (col_scale).
+ *   residual, h, y, rstd, weight : may be NULL; at least one of y and codes must be given.
+ *   weight : [cols] of weight_dtype.  rstd : float[rows].  eps >= 0 (with 0, a row of zeros is NaN).
+ *   codes and exps : both or neither; rounding, seed and step as for gc_act_quant.
+ *   x, residual, h and y share dtype.  h may be x or residual, y may be x or residual (not h too).
+ */
+int gc_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+               int32_t dtype, int64_t rows, int64_t cols, const void* weight,
+               int32_t weight_dtype, float eps, void* h, int64_t ld_h, void* y, int64_t ld_y,
+               float* rstd, int8_t* codes, uint8_t* exps, int32_t rounding, uint64_t seed,
+               uint64_t step, void* stream);
+
+/*
+ * The norm's backward pass from its checkpoint (z the restored values), per row:
+ *   t = dy * weight;  c = sum(t * z) / cols;  dx = round(rstd * (t - z * c) + dres) to dtype,
+ * the gradient of x and of the residual alike; dres is what reaches h by the residual stream.
+ *   dweight (+)= sum over the rows of dy * z  (added to what is there with accumulate != 0)
+ *   dres, weight, dweight : may be NULL.  dx may be dy or dres.
+ *   dweight   : float[cols], any 4-byte alignment (a segment of the flat gradient).
+ *   workspace : 16-byte aligned, of at least gc_rmsnorm_backward_workspace bytes (with dweight;
+ *               else it may be NULL).
+ * A row whose checkpoint restores NaN makes dweight NaN there, also where its dy is 0.
+ */
+int gc_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes /* host */);
+int gc_rmsnorm_backward(const void* dy, int64_t ld_dy, int32_t dtype, int64_t rows, int64_t cols,
+                        const int8_t* codes, const uint8_t* exps, const float* rstd,
+                        const void* weight, int32_t weight_dtype, const void* dres,
+                        int64_t ld_dres, void* dx, int64_t ld_dx, float* dweight, int accumulate,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The weight gradient of a linear layer whose input was kept (z the restored values):
+ *   dweight[n][k] (+)= col_scale[k] * sum over the rows m of dy[m][n] * z[m][k]
+ * with exact products (dy of any type and z are multiplied without rounding either) and fp32
+ * sums; a part of an fp32 dy below 2^-126 may count as 0.
+ *   dy        : rows x n_out of dtype.  col_scale : [cols] of scale_dtype, or NULL (1).
+ *   dweight   : float[n_out][cols], any 4-byte alignment (a segment of the flat gradient);
+ *               added to with accumulate != 0, else overwritten (with 0 for rows = 0).
+ *   workspace : 16-byte aligned, of at least gc_act_weight_grad_workspace bytes (may be NULL
+ *               where that is 0).
+ */
+int gc_act_weight_grad_workspace(int64_t rows, int64_t n_out, int64_t cols, int32_t dtype,
+                                 int64_t* bytes /* host */);
+int gc_act_weight_grad(const void* dy, int64_t ld_dy, int32_t dtype, int64_t rows, int64_t n_out,
+                       int64_t cols, const int8_t* codes, const uint8_t* exps,
+                       const void* col_scale, int32_t scale_dtype, float* dweight, int accumulate,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Forget the threshold estimates (of Top-k calls and the capture floor of threshold calls):
  * the next call runs as on a fresh plan. */
 int gc_plan_reset_estimate(gc_plan* plan, void* stream);

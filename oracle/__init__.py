@@ -56,6 +56,10 @@ def load(path: str):
     L.orc_sign_decompress_segment.restype = None
     L.orc_clip_by_norm_segment.argtypes = [i64, vp, f32, vp]
     L.orc_clip_by_norm_segment.restype = None
+    L.orc_act_quant.argtypes = [i64, i64, vp, ctypes.c_int, u64, u64, vp, vp]
+    L.orc_act_quant.restype = None
+    L.orc_act_restore.argtypes = [i64, i64, vp, vp, vp]
+    L.orc_act_restore.restype = None
     L.orc_decompress_gathered.argtypes = [i32, vp, vp, i32, vp, vp, vp, vp, vp, ctypes.c_int]
     L.orc_decompress_gathered.restype = None
     L.orc_threshold_ef_segment.argtypes = [i64, i64, f32, vp, vp, vp, f32, ctypes.c_int, vp,
@@ -292,3 +296,24 @@ def clip_by_norm_segment(g, c):
     norm = np.empty(1, np.float32)
     lib().orc_clip_by_norm_segment(g.size, _p(g), float(c), _p(norm))
     return norm[0]
+
+
+def act_quant(x, random=False, seed=0, step=0):
+    """8-bit checkpoint of a float32 matrix: (codes int8[rows, pitch], exps uint8[rows,
+    groups])."""
+    _f32(x, "x")
+    rows, cols = x.shape
+    groups = (cols + 31) // 32
+    codes = np.empty((rows, 32 * groups), np.int8)
+    exps = np.empty((rows, groups), np.uint8)
+    lib().orc_act_quant(rows, cols, _p(x), int(bool(random)), int(seed), int(step), _p(codes),
+                        _p(exps))
+    return codes, exps
+
+
+def act_restore(codes, exps, cols):
+    """The float32 values of a checkpoint."""
+    rows = codes.shape[0]
+    out = np.empty((rows, cols), np.float32)
+    lib().orc_act_restore(rows, cols, _p(codes), _p(exps), _p(out))
+    return out

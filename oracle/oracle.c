@@ -566,3 +566,71 @@ void orc_clip_by_norm_segment(int64_t n, float* g, float c, float* norm_out)
         for (int64_t i = 0; i < n; ++i) g[i] = g[i] * f;
     }
 }
+
+/* ------------------------------------------------------------------------------------------
+ * 8-bit activation checkpoint of a rows x cols fp32 matrix (row-major, no gaps): groups of 32
+ * columns share a power of two.  Worked out in double, where every step is exact:
+ *   A = max|x| over the group; e = smallest integer >= -120 with A <= 127 * 2^e (found by trying
+ *   one after the other); a = |x| / 2^e; code = x / 2^e to the nearest integer (ties to even), or
+ *   sign(x) * (floor(a) + [u24 < frac(a) * 2^24]); exps holds e + 127.
+ * A group with a value that is not finite, or with A > 127 * 2^121, gets codes 0 and 255.
+ * codes: int8[rows][pitch], exps: uint8[rows][pitch / 32], pitch = cols rounded up to 32.
+ */
+static uint32_t act_draw24(uint64_t seed, uint64_t step, int64_t i)
+{
+    uint64_t b = (uint64_t)i / 4;
+    uint32_t ctr[4] = {(uint32_t)b, (uint32_t)(b >> 32), (uint32_t)step, 0x54u};
+    uint32_t key[2] = {(uint32_t)seed, (uint32_t)(seed >> 32)};
+    uint32_t r[4];
+    orc_philox4x32_10(ctr, key, r);
+    return r[i % 4] >> 8;
+}
+
+void orc_act_quant(int64_t rows, int64_t cols, const float* x, int random, uint64_t seed,
+                   uint64_t step, int8_t* codes, uint8_t* exps)
+{
+    int64_t groups = (cols + 31) / 32, pitch = 32 * groups;
+    for (int64_t m = 0; m < rows; ++m)
+        for (int64_t g = 0; g < groups; ++g) {
+            int64_t lo = 32 * g, hi = lo + 32 < cols ? lo + 32 : cols;
+            double most = 0.0;
+            int bad = 0;
+            for (int64_t c = lo; c < hi; ++c) {
+                double v = fabs((double)x[m * cols + c]);
+                if (!isfinite(v)) bad = 1;
+                else if (v > most) most = v;
+            }
+            int e = -120;
+            while (!bad && most > ldexp(127.0, e)) ++e;
+            if (e > 121) bad = 1;
+            exps[m * groups + g] = bad ? 255 : (uint8_t)(e + 127);
+            for (int64_t c = lo; c < lo + 32; ++c) {
+                int8_t code = 0;
+                if (c < hi && !bad) {
+                    double v = ldexp((double)x[m * cols + c], -e), a = fabs(v);
+                    if (random) {
+                        double q = floor(a);
+                        double u = (double)act_draw24(seed, step, m * pitch + c);
+                        if (u < (a - q) * 16777216.0) q += 1.0;
+                        code = (int8_t)(v < 0.0 ? -q : q);
+                    } else {
+                        code = (int8_t)nearbyint(v);
+                    }
+                }
+                codes[m * pitch + c] = code;
+            }
+        }
+}
+
+/* out[m][c] = code * 2^(b - 127); NaN where b is 255. */
+void orc_act_restore(int64_t rows, int64_t cols, const int8_t* codes, const uint8_t* exps,
+                     float* out)
+{
+    int64_t groups = (cols + 31) / 32;
+    for (int64_t m = 0; m < rows; ++m)
+        for (int64_t c = 0; c < cols; ++c) {
+            int b = exps[m * groups + c / 32];
+            out[m * cols + c] = b == 255 ? (float)NAN
+                              : (float)ldexp((double)codes[m * groups * 32 + c], b - 127);
+        }
+}
