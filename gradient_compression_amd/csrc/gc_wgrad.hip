@@ -18,107 +18,210 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
-constexpr int kTileN = 128, kTileK = 128, kStep = 32, kThreadsW = 256;
-// 64 bytes past the row: the four rows of a transposing read start in different quarters of the banks
-constexpr int kPitchN = kTileN + 32, kPitchK = kTileK + 32;
-
 // The parts of a value of the type: bf16 1, fp16 2, fp32 3.
 template <int DT>
 constexpr int parts() {
   return DT == kBF16 ? 1 : DT == kF16 ? 2 : 3;
 }
 
+// A workgroup's tile of dW, kTN x kTK, shared by kWN x kWK waves; BM rows of dY and Z a step.
+template <int TN, int TK, int WN, int WK, int BM>
+struct Tile {
+  static constexpr int kTN = TN, kTK = TK, kWN = WN, kWK = WK, kBM = BM;
+  static constexpr int kThreads = 64 * WN * WK;
+  static constexpr int kFN = TN / WN / 32, kFK = TK / WK / 32;   // 32x32 products of a wave
+  // 64 bytes past a row: the four rows of a transposing read start in different quarters of the banks
+  static constexpr int kPitchN = TN + 32, kPitchK = TK + 32;
+  static constexpr int kSlices = BM / 16;   // rows of one matrix instruction
+  static_assert(kThreads == 2 * TN && TN == TK, "a thread stages one octet of a slice");
+};
+
 __device__ __forceinline__ uint32_t pack_high(float a, float b) {   // their upper halves
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
 }
 
-// One 32x32x16 operand of a wave: 8 rows of the tile for each lane's column, read across the rows of LDS.
-__device__ __forceinline__ b8 fragment(const short* base, int pitch) {
-  const int l = lane_id(), b = l >> 4, i = l & 15;
-  const short* p = base + (8 * (b >> 1) + (i >> 2)) * pitch + 16 * (b & 1) + 4 * (i & 3);
+// One 32x32x16 operand of a wave: 8 rows of the slice for each lane's column, read across the
+// rows of LDS.
+__device__ __forceinline__ b8 fragment(const short* p, int pitch) {
   const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
   const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 4 * pitch));
   return __builtin_bit_cast(b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// 8 columns of a row as they lie in memory, zeros where the row or the columns end.
+template <int DT>
+struct Raw {
+  typename Elt<DT>::T v[8];
+};
 template <int DT, bool kVec>
-__global__ __launch_bounds__(kThreadsW) void k_wgrad(WgradArgs a, int splits) {
+__device__ __forceinline__ Raw<DT> load_raw(const typename Elt<DT>::T* p, int col, int cols,
+                                            bool in) {
   typedef typename Elt<DT>::T T;
-  constexpr int NS = parts<DT>();
-  __shared__ __align__(16) short s_y[NS][kStep][kPitchN];
-  __shared__ __align__(16) short s_z[kStep][kPitchK];
-  const int n0 = blockIdx.y * kTileN, k0 = blockIdx.x * kTileK;
-  const int wave = wave_id(), lane = lane_id();
-  const int wn = (wave >> 1) * 64, wk = (wave & 1) * 64;
-  const int groups = (a.cols + kActGroup - 1) / kActGroup, octets = groups * (kActGroup / 8);
-  const int64_t steps = (a.rows + kStep - 1) / kStep;
-  const int64_t first = steps * blockIdx.z / splits, last = steps * (blockIdx.z + 1) / splits;
-  f16v acc[2][2] = {};
-  for (int64_t s = first; s < last; ++s) {
-    const int64_t m0 = s * kStep;
-    __syncthreads();
+  Raw<DT> r;
+  if (kVec && in && col + 8 <= cols) {
+    r = *reinterpret_cast<const Raw<DT>*>(p + col);
+  } else {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int o = threadIdx.x + p * kThreadsW, r = o >> 4, c = (o & 15) * 8;
-      const int64_t m = m0 + r;
-      const bool in = m < a.rows;
-      float v[8] = {};
-      if (in) load8<DT, kVec>(static_cast<const T*>(a.dy.p) + m * a.dy.ld, n0 + c, a.n_out, v);
-      if constexpr (DT == kF32) {   // a NaN whose upper half alone would read as Inf
+    for (int j = 0; j < 8; ++j) r.v[j] = in && col + j < cols ? p[col + j] : (T)0.0f;
+  }
+  return r;
+}
+
+// The bf16 parts of 8 values, part q at y + q * plane.
+template <int DT>
+__device__ __forceinline__ void store_parts(short* y, int plane, const Raw<DT>& r) {
+  if constexpr (DT == kBF16) {
+    *reinterpret_cast<u4*>(y) = __builtin_bit_cast(u4, r);
+  } else {
+    float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (v[j] != v[j]) v[j] = __uint_as_float(0x7FC00000u);
-      }
+    for (int j = 0; j < 8; ++j) {
+      v[j] = to_float(r.v[j]);
+      // a NaN whose upper half alone would read as Inf
+      if (DT == kF32 && v[j] != v[j]) v[j] = __uint_as_float(0x7FC00000u);
+    }
 #pragma unroll
-      for (int q = 0; q < NS; ++q) {
-        u4 w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_high(v[2 * j], v[2 * j + 1]);
-        *reinterpret_cast<u4*>(&s_y[q][r][c]) = w;
-        if (q + 1 < NS)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            // what is left under the 8 bits just taken; nothing is left of Inf and NaN
-            const float top = __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);
-            v[j] = mag_key(v[j]) < 0x7F800000u ? v[j] - top : 0.0f;
-          }
-      }
-      float z[8] = {};
-      const int octet = k0 / 8 + (o & 15);
-      if (in && octet < octets) {
-        const int64_t i = m * octets + octet;
-        decode8(reinterpret_cast<const u2*>(a.codes)[i], exponent_scale(a.exps[i >> 2]), z);
-      }
+    for (int q = 0; q < parts<DT>(); ++q) {
       u4 w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack_high(z[2 * j], z[2 * j + 1]);
-      *reinterpret_cast<u4*>(&s_z[r][c]) = w;
-    }
-    __syncthreads();
+      for (int j = 0; j < 4; ++j) w[j] = pack_high(v[2 * j], v[2 * j + 1]);
+      *reinterpret_cast<u4*>(y + q * plane) = w;
+      if (q + 1 < parts<DT>())
 #pragma unroll
-    for (int mm = 0; mm < kStep; mm += 16) {
-      b8 fz[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) fz[j] = fragment(&s_z[mm][wk + 32 * j], kPitchK);
-#pragma unroll
-      for (int q = 0; q < NS; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const b8 fy = fragment(&s_y[q][mm][wn + 32 * i], kPitchN);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy, fz[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 8; ++j) {
+          // what is left under the 8 bits just taken; nothing is left of Inf and NaN
+          const float top = __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);
+          v[j] = mag_key(v[j]) < 0x7F800000u ? v[j] - top : 0.0f;
         }
     }
   }
-  float* out = splits > 1 ? a.ws + (int64_t)blockIdx.z * a.n_out * a.cols : a.dw;
+}
+
+// Tile of this workgroup.  Workgroups go to the 8 XCDs in turn: each XCD gets a contiguous range of
+// the order below, in which 8 tiles along n share their part of Z, and its L2 holds what they share.
+__device__ __forceinline__ void tile_of(int tiles_n, int tiles_k, int* tn, int* tk) {
+  const int total = tiles_n * tiles_k, id = blockIdx.x;
+  const int q = total / 8, r = total % 8, xcd = id % 8, i = id / 8;
+  const int t = xcd < r ? xcd * (q + 1) + i : r * (q + 1) + (xcd - r) * q + i;
+  const int band = t / (8 * tiles_k), high = min(8, tiles_n - 8 * band);
+  const int in = t - band * 8 * tiles_k;
+  *tn = 8 * band + in % high;
+  *tk = in / high;
+}
+
+template <int DT, bool kVec, typename C>
+__global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int splits) {
+  typedef typename Elt<DT>::T T;
+  constexpr int NS = parts<DT>(), NP = C::kSlices;
+  constexpr int kPlane = C::kBM * C::kPitchN, kStage = NS * kPlane + C::kBM * C::kPitchK;
+  __shared__ __align__(16) short s_mem[2 * kStage];   // two stages: the parts of dY, then Z
+  int tn, tk;
+  tile_of((a.n_out + C::kTN - 1) / C::kTN, (a.cols + C::kTK - 1) / C::kTK, &tn, &tk);
+  const int n0 = tn * C::kTN, k0 = tk * C::kTK;
+  const int wave = wave_id(), lane = lane_id();
+  const int wn = (wave / C::kWK) * (C::kTN / C::kWN), wk = (wave % C::kWK) * (C::kTK / C::kWK);
+  const int octets = (a.cols + kActGroup - 1) / kActGroup * (kActGroup / 8);
+  const int64_t steps = (a.rows + C::kBM - 1) / C::kBM;
+  const int64_t first = steps * blockIdx.y / splits, last = steps * (blockIdx.y + 1) / splits;
+
+  // This thread stages row r, octet c of every slice.
+  const int r = threadIdx.x / (C::kTN / 8), c = threadIdx.x % (C::kTN / 8);
+  const bool has_z = k0 / 8 + c < octets;
+  Raw<DT> y[NP];
+  u2 z[NP];
+  uint32_t e[NP];
+  auto load = [&](int64_t step, int p) {
+    const int64_t m = step * C::kBM + 16 * p + r;
+    const bool in = m < a.rows;
+    y[p] = load_raw<DT, kVec>(static_cast<const T*>(a.dy.p) + m * a.dy.ld, n0 + 8 * c, a.n_out, in);
+    const int64_t i = m * octets + k0 / 8 + c;
+    z[p] = u2{0, 0};
+    e[p] = 0;
+    if (in && has_z) {
+      z[p] = reinterpret_cast<const u2*>(a.codes)[i];
+      e[p] = a.exps[i >> 2];
+    }
+  };
+  auto store = [&](int stage, int p) {
+    short* s = s_mem + stage * kStage;
+    store_parts<DT>(s + (16 * p + r) * C::kPitchN + 8 * c, kPlane, y[p]);
+    float v[8];
+    decode8(z[p], exponent_scale(e[p]), v);
+    u4 w;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 4; ++j) w[j] = pack_high(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<u4*>(s + NS * kPlane + (16 * p + r) * C::kPitchK + 8 * c) = w;
+  };
+  // The lane's place in a transposing read.
+  const int fr = 8 * (lane >> 5) + ((lane & 15) >> 2), fc = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  auto read_z = [&](int stage, int p, b8 (&f)[C::kFK]) {
+    const short* s = s_mem + stage * kStage + NS * kPlane + (16 * p + fr) * C::kPitchK + wk + fc;
+#pragma unroll
+    for (int j = 0; j < C::kFK; ++j) f[j] = fragment(s + 32 * j, C::kPitchK);
+  };
+  auto read_y = [&](int stage, int p, int q, b8 (&f)[C::kFN]) {
+    const short* s = s_mem + stage * kStage + q * kPlane + (16 * p + fr) * C::kPitchN + wn + fc;
+#pragma unroll
+    for (int i = 0; i < C::kFN; ++i) f[i] = fragment(s + 32 * i, C::kPitchN);
+  };
+
+  f16v acc[C::kFN][C::kFK] = {};
+  if (first < last) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) load(first, p);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) store(0, p);
+    if (first + 1 < last)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) load(first + 1, p);
+    __syncthreads();
+  }
+  // Step s multiplies stage s % 2 while the next step's rows, loaded a step ago, go to the other
+  // stage slice by slice and the rows of the step after it are loaded.
+  for (int64_t s = first; s < last; ++s) {
+    const int stage = (int)(s - first) & 1;
+    b8 fz[C::kFK], fy[C::kFN];
+    read_z(stage, 0, fz);
+    read_y(stage, 0, 0, fy);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+#pragma unroll
+      for (int q = 0; q < NS; ++q) {
+        b8 ny[C::kFN], nz[C::kFK];
+        const bool more = q + 1 < NS || p + 1 < NP;
+        if (more) {
+          if (q + 1 == NS) read_z(stage, p + 1, nz);
+          read_y(stage, q + 1 < NS ? p : p + 1, q + 1 < NS ? q + 1 : 0, ny);
+        }
+        if (q == 0) {
+          if (s + 1 < last) store(stage ^ 1, p);
+          if (s + 2 < last) load(s + 2, p);
+        }
+#pragma unroll
+        for (int i = 0; i < C::kFN; ++i)
+#pragma unroll
+          for (int j = 0; j < C::kFK; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy[i], fz[j], acc[i][j], 0, 0, 0);
+        if (more) {
+#pragma unroll
+          for (int i = 0; i < C::kFN; ++i) fy[i] = ny[i];
+          if (q + 1 == NS)
+#pragma unroll
+            for (int j = 0; j < C::kFK; ++j) fz[j] = nz[j];
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  float* out = splits > 1 ? a.ws + (int64_t)blockIdx.y * a.n_out * a.cols : a.dw;
+#pragma unroll
+  for (int j = 0; j < C::kFK; ++j) {
     const int k = k0 + wk + 32 * j + (lane & 31);
     if (k >= a.cols) continue;
     const float sc = splits == 1 && a.col_scale ? load_any(a.col_scale, a.scale_dtype, k) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < C::kFN; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int n = n0 + wn + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
@@ -141,36 +244,63 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a, int splits) {
   a.dw[i] = a.accumulate ? a.dw[i] + v : v;
 }
 
+// 128 KB and a bit of LDS: one workgroup of 8 waves a CU.  Values of several parts take half the rows a step.
 template <int DT>
-void wgrad(const WgradArgs& a, int splits, hipStream_t st) {
-  const dim3 grid(blocks_for(a.cols, kTileK), blocks_for(a.n_out, kTileN), splits);
+using Large = Tile<256, 256, 2, 4, DT == kBF16 ? 64 : 32>;
+template <int DT>
+using Small = Tile<128, 128, 2, 2, DT == kBF16 ? 64 : 32>;
+
+struct Shape {
+  bool large;
+  int splits;
+};
+
+int64_t tiles_of(int32_t n_out, int32_t cols, int t) {
+  return (((int64_t)n_out + t - 1) / t) * (((int64_t)cols + t - 1) / t);
+}
+
+// Large tiles where they fill the 256 CUs; else small ones, the sum over the rows split so that
+// there are about 512 workgroups (two a CU), each of at least 2 steps.
+Shape shape_of(int64_t rows, int32_t n_out, int32_t cols, int dtype) {
+  if (tiles_of(n_out, cols, 256) >= 192) return {true, 1};
+  const int64_t tiles = tiles_of(n_out, cols, 128);
+  const int64_t bm = dtype == kBF16 ? 64 : 32, steps = (rows + bm - 1) / bm;
+  int64_t s = tiles ? 512 / tiles : 1;
+  if (s > steps / 2) s = steps / 2;
+  return {false, s < 1 ? 1 : s > 16 ? 16 : (int)s};
+}
+
+template <int DT, bool kVec, typename C>
+hipError_t wgrad(const WgradArgs& a, int splits, hipStream_t st) {
+  const dim3 grid((unsigned)tiles_of(a.n_out, a.cols, C::kTN), splits);
+  k_wgrad<DT, kVec, C><<<grid, C::kThreads, 0, st>>>(a, splits);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t wgrad(const WgradArgs& a, const Shape& s, hipStream_t st) {
   const bool vec = (reinterpret_cast<uintptr_t>(a.dy.p) & 15) == 0 &&
                    (a.dy.ld * (int64_t)sizeof(typename Elt<DT>::T) & 15) == 0;
-  if (vec)
-    k_wgrad<DT, true><<<grid, kThreadsW, 0, st>>>(a, splits);
-  else
-    k_wgrad<DT, false><<<grid, kThreadsW, 0, st>>>(a, splits);
+  if (s.large)
+    return vec ? wgrad<DT, true, Large<DT>>(a, s.splits, st) : wgrad<DT, false, Large<DT>>(a, s.splits, st);
+  return vec ? wgrad<DT, true, Small<DT>>(a, s.splits, st) : wgrad<DT, false, Small<DT>>(a, s.splits, st);
 }
 
 }  // namespace
 
 int wgrad_splits(int64_t rows, int32_t n_out, int32_t cols, int dtype) {
-  (void)dtype;
-  const int64_t tiles = ((int64_t)n_out + kTileN - 1) / kTileN * (((int64_t)cols + kTileK - 1) / kTileK);
-  const int64_t steps = (rows + kStep - 1) / kStep;
-  int64_t s = tiles ? 512 / tiles : 1;
-  if (s > steps / 4) s = steps / 4;
-  return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+  return shape_of(rows, n_out, cols, dtype).splits;
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t st) {
   if (a.n_out == 0 || a.cols == 0 || (a.rows == 0 && a.accumulate)) return hipSuccess;
-  const int splits = wgrad_splits(a.rows, a.n_out, a.cols, a.dtype);
-  a.dtype == kF32 ? wgrad<kF32>(a, splits, st) : a.dtype == kBF16 ? wgrad<kBF16>(a, splits, st)
-                                                                  : wgrad<kF16>(a, splits, st);
-  if (hipError_t e = hipGetLastError()) return e;
-  if (splits > 1)
-    k_wgrad_join<<<blocks_for((int64_t)a.n_out * a.cols, 256), 256, 0, st>>>(a, splits);
+  const Shape s = shape_of(a.rows, a.n_out, a.cols, a.dtype);
+  if (hipError_t e = a.dtype == kF32    ? wgrad<kF32>(a, s, st)
+                     : a.dtype == kBF16 ? wgrad<kBF16>(a, s, st)
+                                        : wgrad<kF16>(a, s, st))
+    return e;
+  if (s.splits > 1)
+    k_wgrad_join<<<blocks_for((int64_t)a.n_out * a.cols, 256), 256, 0, st>>>(a, s.splits);
   return hipGetLastError();
 }
 

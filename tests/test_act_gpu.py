@@ -417,6 +417,22 @@ def test_weight_grad_matches_the_formula(dtype):
 
 
 @pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_weight_grad_of_many_tiles(dtype):
+    """Matrices that fill the GPU with the largest tiles, whole and ragged ones, sums of no, one, two
+    and several steps."""
+    for n, (rows, n_out, cols) in enumerate([(1, 3600, 3400), (70, 3585, 3600), (129, 3840, 3328),
+                                             (200, 8200, 1800), (64, 300, 30000)]):
+        log(f"[wgrad] {dtype} {rows} {n_out}x{cols}")
+        dy, codes, exps, want = exact_case(rows, n_out, cols, dtype, n)
+        dw = torch.ones(n_out, cols, device="cuda")
+        if n % 2:
+            dy, _ = strided(dy, 5, 3)
+        gca.act_weight_grad(dy, codes, exps, dw, accumulate=True)
+        torch.cuda.synchronize()
+        assert np.array_equal(f64(dw), want + 1.0), f"{rows} {n_out}x{cols}"
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
 def test_weight_grad_of_strided_and_unaligned_rows(dtype):
     for pad in ((3, 0), (8, 0), (0, 1), (8, 8), (40, 5)):
         check_wgrad(150, 200, 100, dtype, 3, pad=pad)
