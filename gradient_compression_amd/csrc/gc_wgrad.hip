@@ -5,6 +5,8 @@
 // the bf16 matrix cores with exact operands: dY in bf16 as it is, in fp16 as two bf16 parts, in
 // fp32 as three (8 bits each, cut off the top one after the other, so that their sum is the value).
 // Products of two bf16 are exact in fp32, the sums are in fp32.
+#include <type_traits>
+
 #include "gc_act_internal.h"
 
 #include "gc_act.h"
@@ -48,22 +50,27 @@ __device__ __forceinline__ b8 fragment(const short* p, int pitch) {
   return __builtin_bit_cast(b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// 8 columns of a row as they lie in memory, zeros where the row or the columns end.
+// 8 columns of a row as they lie in memory; a row may start at any element, which a 16-byte load
+// bears.
 template <int DT>
 struct Raw {
   typename Elt<DT>::T v[8];
 };
-template <int DT, bool kVec>
-__device__ __forceinline__ Raw<DT> load_raw(const typename Elt<DT>::T* p, int col, int cols,
-                                            bool in) {
-  typedef typename Elt<DT>::T T;
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_raw(const void* p) {
   Raw<DT> r;
-  if (kVec && in && col + 8 <= cols) {
-    r = *reinterpret_cast<const Raw<DT>*>(p + col);
-  } else {
+  __builtin_memcpy(&r, p, sizeof r);
+  return r;
+}
+// The same where the row (in) or its columns may end: zeros past them.
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_edge(const typename Elt<DT>::T* p, int col, int cols,
+                                             bool in) {
+  typedef typename Elt<DT>::T T;
+  if (in && col + 8 <= cols) return load_raw<DT>(p + col);
+  Raw<DT> r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r.v[j] = in && col + j < cols ? p[col + j] : (T)0.0f;
-  }
+  for (int j = 0; j < 8; ++j) r.v[j] = in && col + j < cols ? p[col + j] : (T)0.0f;
   return r;
 }
 
@@ -109,10 +116,10 @@ __device__ __forceinline__ void tile_of(int tiles_n, int tiles_k, int* tn, int* 
   *tk = in / high;
 }
 
-template <int DT, bool kVec, typename C>
+template <int DT, typename C>
 __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int splits) {
   typedef typename Elt<DT>::T T;
-  constexpr int NS = parts<DT>(), NP = C::kSlices;
+  constexpr int NS = parts<DT>(), NP = C::kSlices, kPieces = NS * NP;
   constexpr int kPlane = C::kBM * C::kPitchN, kStage = NS * kPlane + C::kBM * C::kPitchK;
   __shared__ __align__(16) short s_mem[2 * kStage];   // two stages: the parts of dY, then Z
   int tn, tk;
@@ -120,98 +127,138 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
   const int n0 = tn * C::kTN, k0 = tk * C::kTK;
   const int wave = wave_id(), lane = lane_id();
   const int wn = (wave / C::kWK) * (C::kTN / C::kWN), wk = (wave % C::kWK) * (C::kTK / C::kWK);
-  const int octets = (a.cols + kActGroup - 1) / kActGroup * (kActGroup / 8);
+  const int groups = (a.cols + kActGroup - 1) / kActGroup, octets = groups * (kActGroup / 8);
+  const int64_t ld = a.dy.ld;
   const int64_t steps = (a.rows + C::kBM - 1) / C::kBM;
   const int64_t first = steps * blockIdx.y / splits, last = steps * (blockIdx.y + 1) / splits;
+  // Steps whose rows are all there and whose 16-byte loads stay inside dY whatever their column: a
+  // load that starts in a row before the last one ends before the matrix does.  The lanes of
+  // columns past n_out or the pitch read some other column there; what they add up is not stored.
+  const bool wide = n0 + C::kTN <= a.n_out;
+  const int64_t whole = ld < 8 || ld > (1 << 24) || octets > (1 << 22) ? 0
+                        : (wide ? a.rows : a.rows - 1) / C::kBM;
 
   // This thread stages row r, octet c of every slice.
   const int r = threadIdx.x / (C::kTN / 8), c = threadIdx.x % (C::kTN / 8);
+  const int my_octet = min(k0 / 8 + c, octets - 1);
   const bool has_z = k0 / 8 + c < octets;
+  const uint32_t y_off = (uint32_t)(r * ld + min(n0 + 8 * c, a.n_out - 1)) * (uint32_t)sizeof(T);
+  const uint32_t z_off = (uint32_t)(r * octets + my_octet) * 8u;
+  const uint32_t e_off = (uint32_t)(r * groups + (my_octet >> 2));
   Raw<DT> y[NP];
   u2 z[NP];
   uint32_t e[NP];
-  auto load = [&](int64_t step, int p) {
+  auto load_whole = [&](int64_t step, int p) {
+    const int64_t m = step * C::kBM + 16 * p;   // the same in all lanes
+    y[p] = load_raw<DT>(static_cast<const char*>(a.dy.p) + m * ld * (int64_t)sizeof(T) + y_off);
+    z[p] = *reinterpret_cast<const u2*>(reinterpret_cast<const char*>(a.codes) + m * octets * 8 + z_off);
+    e[p] = (a.exps + m * groups)[e_off];
+  };
+  auto load_any_rows = [&](int64_t step, int p) {
     const int64_t m = step * C::kBM + 16 * p + r;
     const bool in = m < a.rows;
-    y[p] = load_raw<DT, kVec>(static_cast<const T*>(a.dy.p) + m * a.dy.ld, n0 + 8 * c, a.n_out, in);
-    const int64_t i = m * octets + k0 / 8 + c;
+    y[p] = load_edge<DT>(static_cast<const T*>(a.dy.p) + m * ld, n0 + 8 * c, a.n_out, in);
     z[p] = u2{0, 0};
     e[p] = 0;
     if (in && has_z) {
+      const int64_t i = m * octets + k0 / 8 + c;
       z[p] = reinterpret_cast<const u2*>(a.codes)[i];
       e[p] = a.exps[i >> 2];
     }
   };
-  auto store = [&](int stage, int p) {
-    short* s = s_mem + stage * kStage;
-    store_parts<DT>(s + (16 * p + r) * C::kPitchN + 8 * c, kPlane, y[p]);
-    float v[8];
-    decode8(z[p], exponent_scale(e[p]), v);
+  auto store = [&](short* stage, int p) {
+    store_parts<DT>(stage + (16 * p + r) * C::kPitchN + 8 * c, kPlane, y[p]);
+    // u = code + 128 is a byte, which one instruction makes a float; u * scale - 128 * scale is the
+    // restored value without a rounding (and NaN for a bad group: Inf - Inf)
+    const float scale = exponent_scale(e[p]), shift = -128.0f * scale;
     u4 w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack_high(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<u4*>(s + NS * kPlane + (16 * p + r) * C::kPitchK + 8 * c) = w;
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t u = z[p][h] ^ 0x80808080u;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = fmaf((float)((u >> (8 * j)) & 0xFFu), scale, shift);
+      w[2 * h] = pack_high(v[0], v[1]);
+      w[2 * h + 1] = pack_high(v[2], v[3]);
+    }
+    *reinterpret_cast<u4*>(stage + NS * kPlane + (16 * p + r) * C::kPitchK + 8 * c) = w;
   };
   // The lane's place in a transposing read.
   const int fr = 8 * (lane >> 5) + ((lane & 15) >> 2), fc = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  auto read_z = [&](int stage, int p, b8 (&f)[C::kFK]) {
-    const short* s = s_mem + stage * kStage + NS * kPlane + (16 * p + fr) * C::kPitchK + wk + fc;
+  const int fz_at = NS * kPlane + fr * C::kPitchK + wk + fc, fy_at = fr * C::kPitchN + wn + fc;
+  auto read_z = [&](const short* stage, int p, b8 (&f)[C::kFK]) {
 #pragma unroll
-    for (int j = 0; j < C::kFK; ++j) f[j] = fragment(s + 32 * j, C::kPitchK);
+    for (int j = 0; j < C::kFK; ++j)
+      f[j] = fragment(stage + fz_at + 16 * p * C::kPitchK + 32 * j, C::kPitchK);
   };
-  auto read_y = [&](int stage, int p, int q, b8 (&f)[C::kFN]) {
-    const short* s = s_mem + stage * kStage + q * kPlane + (16 * p + fr) * C::kPitchN + wn + fc;
+  auto read_y = [&](const short* stage, int p, int q, b8 (&f)[C::kFN]) {
 #pragma unroll
-    for (int i = 0; i < C::kFN; ++i) f[i] = fragment(s + 32 * i, C::kPitchN);
+    for (int i = 0; i < C::kFN; ++i)
+      f[i] = fragment(stage + fy_at + q * kPlane + 16 * p * C::kPitchN + 32 * i, C::kPitchN);
   };
 
   f16v acc[C::kFN][C::kFK] = {};
-  if (first < last) {
+  b8 fz[C::kFK], fy[C::kFN];
+  short *cur = s_mem, *nxt = s_mem + kStage;
+  // One step: its slices are multiplied, each piece (a slice, a part of dY) while the operands of
+  // the next are read.  The next step's rows, loaded a step ago, go to the other stage during all
+  // pieces but the last, and the rows of the step after it are loaded.  Before the last piece all
+  // waves meet: the other stage is complete then, and nobody reads this one any more.
+  auto step = [&](int64_t s, auto all) {
+    const bool more1 = all || s + 1 < last, more2 = all || s + 2 < last;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) load(first, p);
-#pragma unroll
-    for (int p = 0; p < NP; ++p) store(0, p);
-    if (first + 1 < last)
-#pragma unroll
-      for (int p = 0; p < NP; ++p) load(first + 1, p);
-    __syncthreads();
-  }
-  // Step s multiplies stage s % 2 while the next step's rows, loaded a step ago, go to the other
-  // stage slice by slice and the rows of the step after it are loaded.
-  for (int64_t s = first; s < last; ++s) {
-    const int stage = (int)(s - first) & 1;
-    b8 fz[C::kFK], fy[C::kFN];
-    read_z(stage, 0, fz);
-    read_y(stage, 0, 0, fy);
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-#pragma unroll
-      for (int q = 0; q < NS; ++q) {
-        b8 ny[C::kFN], nz[C::kFK];
-        const bool more = q + 1 < NS || p + 1 < NP;
-        if (more) {
-          if (q + 1 == NS) read_z(stage, p + 1, nz);
-          read_y(stage, q + 1 < NS ? p : p + 1, q + 1 < NS ? q + 1 : 0, ny);
-        }
-        if (q == 0) {
-          if (s + 1 < last) store(stage ^ 1, p);
-          if (s + 2 < last) load(s + 2, p);
-        }
-#pragma unroll
-        for (int i = 0; i < C::kFN; ++i)
-#pragma unroll
-          for (int j = 0; j < C::kFK; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy[i], fz[j], acc[i][j], 0, 0, 0);
-        if (more) {
-#pragma unroll
-          for (int i = 0; i < C::kFN; ++i) fy[i] = ny[i];
-          if (q + 1 == NS)
-#pragma unroll
-            for (int j = 0; j < C::kFK; ++j) fz[j] = nz[j];
+    for (int i = 0; i < kPieces; ++i) {
+      const int p = i / NS, q = i % NS;
+      b8 ny[C::kFN], nz[C::kFK];
+      if (i + 1 < kPieces) {
+        if (q + 1 == NS) read_z(cur, p + 1, nz);
+        read_y(cur, (i + 1) / NS, (i + 1) % NS, ny);
+      } else {
+        __syncthreads();
+        if (more1) {
+          read_z(nxt, 0, nz);
+          read_y(nxt, 0, 0, ny);
         }
       }
+#pragma unroll
+      for (int t = 0; t < NP; ++t)
+        if (t * (kPieces - 1) / NP == i) {
+          if (more1) store(nxt, t);
+          if (all)
+            load_whole(s + 2, t);
+          else if (more2)
+            load_any_rows(s + 2, t);
+        }
+#pragma unroll
+      for (int u = 0; u < C::kFN; ++u)
+#pragma unroll
+        for (int j = 0; j < C::kFK; ++j)
+          acc[u][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy[u], fz[j], acc[u][j], 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < C::kFN; ++u) fy[u] = ny[u];
+      if (q + 1 == NS)
+#pragma unroll
+        for (int j = 0; j < C::kFK; ++j) fz[j] = nz[j];
     }
+    short* t = cur;
+    cur = nxt;
+    nxt = t;
+  };
+  if (first < last) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) load_any_rows(first, p);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) store(cur, p);
+    if (first + 1 < last)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) load_any_rows(first + 1, p);
     __syncthreads();
+    read_z(cur, 0, fz);
+    read_y(cur, 0, 0, fy);
+    const int64_t lim = whole < last ? whole : last;
+    int64_t s = first;
+    for (; s + 2 < lim; ++s) step(s, std::true_type());
+    for (; s < last; ++s) step(s, std::false_type());
   }
 
   float* out = splits > 1 ? a.ws + (int64_t)blockIdx.y * a.n_out * a.cols : a.dw;
@@ -270,20 +317,16 @@ Shape shape_of(int64_t rows, int32_t n_out, int32_t cols, int dtype) {
   return {false, s < 1 ? 1 : s > 16 ? 16 : (int)s};
 }
 
-template <int DT, bool kVec, typename C>
+template <int DT, typename C>
 hipError_t wgrad(const WgradArgs& a, int splits, hipStream_t st) {
   const dim3 grid((unsigned)tiles_of(a.n_out, a.cols, C::kTN), splits);
-  k_wgrad<DT, kVec, C><<<grid, C::kThreads, 0, st>>>(a, splits);
+  k_wgrad<DT, C><<<grid, C::kThreads, 0, st>>>(a, splits);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t wgrad(const WgradArgs& a, const Shape& s, hipStream_t st) {
-  const bool vec = (reinterpret_cast<uintptr_t>(a.dy.p) & 15) == 0 &&
-                   (a.dy.ld * (int64_t)sizeof(typename Elt<DT>::T) & 15) == 0;
-  if (s.large)
-    return vec ? wgrad<DT, true, Large<DT>>(a, s.splits, st) : wgrad<DT, false, Large<DT>>(a, s.splits, st);
-  return vec ? wgrad<DT, true, Small<DT>>(a, s.splits, st) : wgrad<DT, false, Small<DT>>(a, s.splits, st);
+  return s.large ? wgrad<DT, Large<DT>>(a, s.splits, st) : wgrad<DT, Small<DT>>(a, s.splits, st);
 }
 
 }  // namespace
