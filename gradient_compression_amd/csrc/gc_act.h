@@ -43,32 +43,70 @@ __device__ __forceinline__ float to_float(__bf16 x) {
   return __uint_as_float((uint32_t)__builtin_bit_cast(uint16_t, x) << 16);
 }
 
-// One value of a vector over the columns whose type is only known at run time.
+// 8 values as they lie in memory, kept in whole registers.  They may start at any element: a
+// 16-byte load bears that.
+template <int DT>
+struct Raw {
+  static constexpr int kWords = sizeof(typename Elt<DT>::T) / 2;   // of 16 bytes
+  u4 w[kWords];
+};
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_raw(const void* p) {
+  Raw<DT> r;
+  __builtin_memcpy(&r, p, sizeof r);
+  return r;
+}
+// 8 columns from col of the row at p, zeros from `cols` on.
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_raw(const typename Elt<DT>::T* p, int col, int cols) {
+  if (col + 8 <= cols) return load_raw<DT>(p + col);
+  Raw<DT> r = {};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (col + j >= cols) continue;
+    if constexpr (sizeof(typename Elt<DT>::T) == 2)
+      r.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[col + j]) << (16 * (j % 2));
+    else
+      r.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, p[col + j]);
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void to_float8(const Raw<DT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (DT == kF32)
+      v[j] = __uint_as_float(r.w[j / 4][j % 4]);
+    else if constexpr (DT == kBF16)
+      v[j] = __uint_as_float(j % 2 ? r.w[0][j / 2] & 0xFFFF0000u : r.w[0][j / 2] << 16);
+    else
+      v[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.w[0][j / 2] >> (16 * (j % 2))));
+  }
+}
+template <int DT>
+__device__ __forceinline__ void load8(const typename Elt<DT>::T* p, int col, int cols,
+                                      float (&v)[8]) {
+  to_float8<DT>(load_raw<DT>(p, col, cols), v);
+}
+
+// One value, and 8, of a vector over the columns whose type is only known at run time; ones for
+// no vector.
 __device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
   return dtype == kF32    ? static_cast<const float*>(p)[i]
          : dtype == kBF16 ? to_float(static_cast<const __bf16*>(p)[i])
                           : (float)static_cast<const _Float16*>(p)[i];
 }
-
-// 8 columns from col of the row at p.  kVec: p and the row pitch are multiples of 16 bytes, so
-// a whole octet is loaded in 16-byte pieces.  Columns from `cols` on give 0.
-template <int DT, bool kVec>
-__device__ __forceinline__ void load8(const typename Elt<DT>::T* p, int col, int cols,
-                                      float (&v)[8]) {
-  typedef typename Elt<DT>::T T;
-  if (kVec && col + 8 <= cols) {
-    T raw[8];
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<u4*>(raw) = *reinterpret_cast<const u4*>(p + col);
-    } else {
-      reinterpret_cast<u4*>(raw)[0] = reinterpret_cast<const u4*>(p + col)[0];
-      reinterpret_cast<u4*>(raw)[1] = reinterpret_cast<const u4*>(p + col)[1];
-    }
+__device__ __forceinline__ void load8_any(const void* p, int dtype, int col, int cols,
+                                          float (&v)[8]) {
+  if (!p) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = to_float(raw[j]);
+    for (int j = 0; j < 8; ++j) v[j] = 1.0f;
+  } else if (dtype == kF32) {
+    load8<kF32>(static_cast<const float*>(p), col, cols, v);
+  } else if (dtype == kBF16) {
+    load8<kBF16>(static_cast<const __bf16*>(p), col, cols, v);
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = col + j < cols ? to_float(p[col + j]) : 0.0f;
+    load8<kF16>(static_cast<const _Float16*>(p), col, cols, v);
   }
 }
 
@@ -82,24 +120,18 @@ __device__ __forceinline__ typename Elt<DT>::T round_to(float x) {
 }
 
 // Rounds v to the type and stores the columns below `cols`.
-template <int DT, bool kVec>
+template <int DT>
 __device__ __forceinline__ void store8(typename Elt<DT>::T* p, int col, int cols,
                                        const float (&v)[8]) {
-  typedef typename Elt<DT>::T T;
-  if (kVec && col + 8 <= cols) {
-    T raw[8];
+  typename Elt<DT>::T raw[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) raw[j] = round_to<DT>(v[j]);
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<u4*>(p + col) = *reinterpret_cast<u4*>(raw);
-    } else {
-      reinterpret_cast<u4*>(p + col)[0] = reinterpret_cast<u4*>(raw)[0];
-      reinterpret_cast<u4*>(p + col)[1] = reinterpret_cast<u4*>(raw)[1];
-    }
+  for (int j = 0; j < 8; ++j) raw[j] = round_to<DT>(v[j]);
+  if (col + 8 <= cols) {
+    __builtin_memcpy(p + col, raw, sizeof raw);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (col + j < cols) p[col + j] = round_to<DT>(v[j]);
+      if (col + j < cols) p[col + j] = raw[j];
   }
 }
 

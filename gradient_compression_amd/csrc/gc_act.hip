@@ -40,7 +40,7 @@ __device__ __forceinline__ bool place(const RowMap& m, int64_t u, int64_t* row, 
   return *row < m.rows && *octet < m.octets;
 }
 
-template <int DT, bool kVec, bool kRandom>
+template <int DT, bool kRandom>
 __global__ __launch_bounds__(kThreadsAct) void k_act_quant(RowMap m,
                                                            const typename Elt<DT>::T* x,
                                                            int64_t ld, ActRound r, int8_t* codes,
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kThreadsAct) void k_act_quant(RowMap m,
   int octet;
   if (!place(m, u, &row, &octet)) return;   // whole quads at a time
   float v[8];
-  load8<DT, kVec>(x + row * ld, octet * 8, m.cols, v);
+  load8<DT>(x + row * ld, octet * 8, m.cols, v);
   const int64_t i = (row * m.octets + octet);
   uint32_t e;
   const u2 q = encode8<kRandom>(v, (uint64_t)i * 2, r.seed_lo, r.seed_hi, r.step_lo, &e);
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kThreadsAct) void k_act_quant(RowMap m,
   if ((octet & 3) == 0) exps[i >> 2] = (uint8_t)e;
 }
 
-template <int DT, bool kVec>
+template <int DT>
 __global__ __launch_bounds__(kThreadsAct) void k_act_restore(RowMap m, const int8_t* codes,
                                                              const uint8_t* exps,
                                                              typename Elt<DT>::T* out,
@@ -70,32 +70,18 @@ __global__ __launch_bounds__(kThreadsAct) void k_act_restore(RowMap m, const int
   const int64_t i = row * m.octets + octet;
   float v[8];
   decode8(reinterpret_cast<const u2*>(codes)[i], exponent_scale(exps[i >> 2]), v);
-  store8<DT, kVec>(out + row * ld, octet * 8, m.cols, v);
-}
-
-bool vectors(const Mat& a, int dtype) {
-  const int64_t bytes = dtype == kF32 ? 4 : 2;
-  return (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && (a.ld * bytes & 15) == 0;
-}
-
-template <int DT, bool kVec>
-void quant(const RowMap& m, const Mat& x, const ActRound& r, int8_t* codes, uint8_t* exps,
-           hipStream_t st) {
-  typedef const typename Elt<DT>::T* P;
-  const unsigned grid = blocks_for(m.units, kThreadsAct / 64);
-  if (r.random)
-    k_act_quant<DT, kVec, true><<<grid, kThreadsAct, 0, st>>>(m, (P)x.p, x.ld, r, codes, exps);
-  else
-    k_act_quant<DT, kVec, false><<<grid, kThreadsAct, 0, st>>>(m, (P)x.p, x.ld, r, codes, exps);
+  store8<DT>(out + row * ld, octet * 8, m.cols, v);
 }
 
 template <int DT>
 void quant(const RowMap& m, const Mat& x, const ActRound& r, int8_t* codes, uint8_t* exps,
            hipStream_t st) {
-  if (vectors(x, DT))
-    quant<DT, true>(m, x, r, codes, exps, st);
+  typedef const typename Elt<DT>::T* P;
+  const unsigned grid = blocks_for(m.units, kThreadsAct / 64);
+  if (r.random)
+    k_act_quant<DT, true><<<grid, kThreadsAct, 0, st>>>(m, (P)x.p, x.ld, r, codes, exps);
   else
-    quant<DT, false>(m, x, r, codes, exps, st);
+    k_act_quant<DT, false><<<grid, kThreadsAct, 0, st>>>(m, (P)x.p, x.ld, r, codes, exps);
 }
 
 template <int DT>
@@ -103,10 +89,7 @@ void restore(const RowMap& m, const int8_t* codes, const uint8_t* exps, const Ma
              hipStream_t st) {
   typedef typename Elt<DT>::T* P;
   const unsigned grid = blocks_for(m.units, kThreadsAct / 64);
-  if (vectors(out, DT))
-    k_act_restore<DT, true><<<grid, kThreadsAct, 0, st>>>(m, codes, exps, (P)out.p, out.ld);
-  else
-    k_act_restore<DT, false><<<grid, kThreadsAct, 0, st>>>(m, codes, exps, (P)out.p, out.ld);
+  k_act_restore<DT><<<grid, kThreadsAct, 0, st>>>(m, codes, exps, (P)out.p, out.ld);
 }
 
 }  // namespace

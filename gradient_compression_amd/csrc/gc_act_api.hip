@@ -185,7 +185,7 @@ int gc_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
   if (!bytes) return GC_ERR_INVALID_ARG;
   if (int rc = check_sizes(rows, cols)) return rc;
   if (cols > gc::kNormMostCols) return GC_ERR_UNSUPPORTED;
-  *bytes = gc::norm_grad_workers(rows, (int32_t)cols) * groups_of(cols) * 32 * 4;
+  *bytes = gc::norm_grad_blocks(rows, (int32_t)cols) * groups_of(cols) * 32 * 4;
   return GC_OK;
 }
 

@@ -45,7 +45,7 @@ struct NormGradArgs {
   const void* weight;          // or null
   float* dweight;              // [cols] or null
   int accumulate;
-  float* ws;                   // [workers][pitch] partial sums, with dweight
+  float* ws;                   // [blocks][pitch] partial sums, with dweight
 };
 
 struct WgradArgs {
@@ -68,8 +68,8 @@ hipError_t launch_act_quant(const Mat& x, int dtype, int64_t rows, int32_t cols,
 hipError_t launch_act_restore(const int8_t* codes, const uint8_t* exps, int64_t rows,
                               int32_t cols, const Mat& out, int dtype, hipStream_t st);
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
-// Rows of partial sums that a backward call with a weight gradient writes.
-int64_t norm_grad_workers(int64_t rows, int32_t cols);
+// Blocks of a backward call, each of which writes a row of partial sums of the weight gradient.
+int64_t norm_grad_blocks(int64_t rows, int32_t cols);
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t st);
 // Parts into which a weight gradient's sum over the rows is split.
 int wgrad_splits(int64_t rows, int32_t n_out, int32_t cols, int dtype);

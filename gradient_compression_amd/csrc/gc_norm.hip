@@ -40,7 +40,7 @@ constexpr int block_threads() {
   return TPR == 64 ? 256 : TPR;
 }
 
-template <int DT, bool kVec, bool kRandom, int TPR, int NV>
+template <int DT, bool kRandom, int TPR, int NV>
 __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm(NormArgs a) {
   typedef typename Elt<DT>::T T;
   __shared__ double s_part[16];
@@ -54,44 +54,47 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm(NormArgs a) {
   T* hp = a.h.p ? static_cast<T*>(a.h.p) + row * a.h.ld : nullptr;
   T* yp = a.y.p ? static_cast<T*>(a.y.p) + row * a.y.ld : nullptr;
 
-  float h[NV][8];
+  float h[NV][8], w[NV][8];
   double ss = 0.0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int col = (t + v * TPR) * 8;
-    load8<DT, kVec>(x, col, cols, h[v]);
+    load8<DT>(x, col, cols, h[v]);
   }
   if (res) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int col = (t + v * TPR) * 8;
       float r[8];
-      load8<DT, kVec>(res, col, cols, r);
+      load8<DT>(res, col, cols, r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[v][j] = to_float(round_to<DT>(h[v][j] + r[j]));
     }
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (hp) store8<DT, kVec>(hp, (t + v * TPR) * 8, cols, h[v]);
+    if (hp) store8<DT>(hp, (t + v * TPR) * 8, cols, h[v]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)h[v][j], (double)h[v][j], ss);
   }
+  if (yp)
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      load8_any(a.weight, a.weight_dtype, (t + v * TPR) * 8, cols, w[v]);
   ss = row_sum<TPR>(ss, s_part);
   const float rstd = (float)(1.0 / sqrt(ss / (double)cols + (double)a.eps));
   if (t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int octet = t + v * TPR, col = octet * 8;
-    float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[v][j] = h[v][j] * rstd;
-      const float w = a.weight && col + j < cols ? load_any(a.weight, a.weight_dtype, col + j)
-                                                 : 1.0f;
-      y[j] = h[v][j] * w;
+    for (int j = 0; j < 8; ++j) h[v][j] = h[v][j] * rstd;
+    if (yp) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = h[v][j] * w[v][j];
+      store8<DT>(yp, col, cols, y);
     }
-    if (yp) store8<DT, kVec>(yp, col, cols, y);
     if (a.codes && octet < octets) {   // whole quads at a time
       // columns past the row hold 0 * rstd: 0, or NaN where rstd is Inf, which must not reach
       // the last group's scale
@@ -109,97 +112,171 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm(NormArgs a) {
   }
 }
 
-template <int DT, bool kVec, int TPR, int NV>
-__global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormGradArgs a,
-                                                                           int64_t workers) {
+// What a thread holds of one row of the backward pass, as it lies in memory.
+template <int DT, int NV>
+struct GradRow {
+  Raw<DT> dy[NV], dres[NV];
+  u2 codes[NV];
+  uint32_t exps[NV];
+  float rstd;
+};
+
+// A worker (a wave or a block, as in the forward pass) takes the rows worker, worker + workers, ...
+// Its threads keep their columns' partial sums of dw in registers, and their weights and the next
+// row, loaded before the current one is reduced, where the registers last (up to 4 and up to 2
+// octets a thread).  A row is held as it was loaded and expanded twice: its floats would cost half
+// of the waves.
+template <int DT, int TPR, int NV>
+__global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormGradArgs a) {
   typedef typename Elt<DT>::T T;
-  __shared__ float s_part[16];
-  constexpr int kRows = block_threads<TPR>() / TPR;
+  constexpr int kRows = block_threads<TPR>() / TPR, kWavesN = TPR / 64;
+  constexpr bool kAhead = NV <= 2, kKeepW = NV <= 4;
+  __shared__ float s_part[2][kWavesN];
+  __shared__ float s_dw[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * NV * 8 : 1];
   const int t = TPR == 64 ? lane_id() : threadIdx.x;
+  const int64_t workers = (int64_t)gridDim.x * kRows;
   const int64_t worker = (int64_t)blockIdx.x * kRows + (TPR == 64 ? wave_id() : 0);
-  if (worker >= workers) return;   // a whole wave (TPR 64) or nobody
   const int cols = a.cols, octets = (cols + kActGroup - 1) / kActGroup * (kActGroup / 8);
-  float dw[NV][8] = {};
-  for (int64_t row = worker; row < a.rows; row += workers) {
+  const bool has_res = a.dres.p != nullptr;
+
+  float dw[NV][8] = {}, w[kKeepW ? NV : 1][8];
+  if (kKeepW)
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      load8_any(a.weight, a.weight_dtype, (t + v * TPR) * 8, cols, w[v]);
+  auto load = [&](int64_t row, GradRow<DT, NV>& r) {
     const T* dy = static_cast<const T*>(a.dy.p) + row * a.dy.ld;
-    const T* dres = a.dres.p ? static_cast<const T*>(a.dres.p) + row * a.dres.ld : nullptr;
-    T* dx = static_cast<T*>(a.dx.p) + row * a.dx.ld;
-    float g[NV][8], z[NV][8];
-    float s = 0.0f;
+    const T* dres = static_cast<const T*>(a.dres.p) + row * a.dres.ld;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int octet = t + v * TPR, col = octet * 8;
-      load8<DT, kVec>(dy, col, cols, g[v]);
+      r.dy[v] = load_raw<DT>(dy, col, cols);
+      if (has_res) r.dres[v] = load_raw<DT>(dres, col, cols);
+      r.codes[v] = u2{0, 0};
+      r.exps[v] = 0;
       if (octet < octets) {
         const int64_t i = row * octets + octet;
-        decode8(reinterpret_cast<const u2*>(a.codes)[i], exponent_scale(a.exps[i >> 2]), z[v]);
+        r.codes[v] = reinterpret_cast<const u2*>(a.codes)[i];
+        r.exps[v] = a.exps[i >> 2];
       }
-      // the padding of the last octets is not part of the row, whatever its group restores to
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col + j >= cols) z[v][j] = 0.0f;
     }
+    r.rstd = a.rstd[row];
+  };
+  // z of octet v; the padding of the last octets is not part of the row, whatever its group
+  // restores to
+  auto restored = [&](const GradRow<DT, NV>& r, int v, float (&z)[8]) {
+    decode8(r.codes[v], exponent_scale(r.exps[v]), z);
+    const int col = (t + v * TPR) * 8;
+    if (col + 8 > cols)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = col + j < cols ? z[j] : 0.0f;
+  };
+
+  GradRow<DT, NV> cur, nxt;
+  int turn = 0;
+  if (worker < a.rows) load(worker, cur);
+  for (int64_t row = worker; row < a.rows; row += workers) {
+    if (kAhead && row + workers < a.rows) load(row + workers, nxt);
+    if (!kAhead && row != worker) load(row, cur);
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float g[8], z[8];
+      to_float8<DT>(cur.dy[v], g);
+      restored(cur, v, z);
+      if (!kKeepW) load8_any(a.weight, a.weight_dtype, (t + v * TPR) * 8, cols, w[0]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[v][j] = fmaf(g[j], z[j], dw[v][j]);
+        s = fmaf(g[j] * w[kKeepW ? v : 0][j], z[j], s);
+      }
+    }
+    // the waves' sums alternate between two places, so that one meeting a row is enough
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
+    if (kWavesN > 1) {
+      if (lane_id() == 0) s_part[turn][wave_id()] = s;
+      __syncthreads();
+      s = s_part[turn][0];
+#pragma unroll
+      for (int i = 1; i < kWavesN; ++i) s += s_part[turn][i];
+      turn ^= 1;
+    }
+    const float c = s / (float)cols;
+    // what was loaded made opaque, or the compiler keeps the floats of the first expansion instead
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      asm("" : "+v"(cur.codes[v]), "+v"(cur.exps[v]));
+#pragma unroll
+      for (int j = 0; j < Raw<DT>::kWords; ++j) asm("" : "+v"(cur.dy[v].w[j]));
+    }
+    T* dx = static_cast<T*>(a.dx.p) + row * a.dx.ld;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int col = (t + v * TPR) * 8;
+      float g[8], z[8], r[8];
+      to_float8<DT>(cur.dy[v], g);
+      restored(cur, v, z);
+      if (!kKeepW) load8_any(a.weight, a.weight_dtype, col, cols, w[0]);
+      if (has_res) to_float8<DT>(cur.dres[v], r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dw[v][j] = fmaf(g[v][j], z[v][j], dw[v][j]);
-        const float w = a.weight && col + j < cols ? load_any(a.weight, a.weight_dtype, col + j)
-                                                   : 1.0f;
-        g[v][j] = g[v][j] * w;
-        s = fmaf(g[v][j], z[v][j], s);
+        const float d = cur.rstd * fmaf(-z[j], c, g[j] * w[kKeepW ? v : 0][j]);
+        g[j] = has_res ? d + r[j] : d;
       }
+      store8<DT>(dx, col, cols, g);
     }
-    const float c = row_sum<TPR>(s, s_part) / (float)cols;
-    const float rstd = a.rstd[row];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int col = (t + v * TPR) * 8;
-      float r[8];
-      if (dres) load8<DT, kVec>(dres, col, cols, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = rstd * fmaf(-z[v][j], c, g[v][j]);
-        g[v][j] = dres ? d + r[j] : d;
-      }
-      store8<DT, kVec>(dx, col, cols, g[v]);
-    }
+    if (kAhead) cur = nxt;
   }
   if (!a.dweight) return;
+  // One row of partial sums a block: the waves of a block with several workers are joined first.
+  if (kRows > 1) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s_dw[wave_id()][(v * 8 + j) * 64 + t] = dw[v][j];
+    __syncthreads();
+    if (wave_id() != 0) return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 1; i < kRows; ++i) dw[v][j] += s_dw[i][(v * 8 + j) * 64 + t];
+  }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int octet = t + v * TPR;
     if (octet >= octets) continue;
-    f4* p = reinterpret_cast<f4*>(a.ws + (worker * octets + octet) * 8);
+    f4* p = reinterpret_cast<f4*>(a.ws + ((int64_t)blockIdx.x * octets + octet) * 8);
     p[0] = f4{dw[v][0], dw[v][1], dw[v][2], dw[v][3]};
     p[1] = f4{dw[v][4], dw[v][5], dw[v][6], dw[v][7]};
   }
 }
 
-// dw[k] (+)= the workers' partial sums, added in a fixed order: slice s of 32 sums the workers
-// s, s + 32, ... of a column, then the slices are joined.
-__global__ __launch_bounds__(1024) void k_norm_dweight(const float* ws, int64_t workers,
-                                                       int32_t pitch, int32_t cols, float* dw,
-                                                       int accumulate) {
-  __shared__ float s_sum[32][33];
-  const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + c;    // below pitch, a multiple of 32
-  float acc = 0.0f;
-  for (int64_t i = s; i < workers; i += 32) acc += ws[i * pitch + col];
-  s_sum[s][c] = acc;
-  __syncthreads();
-  if (s == 0 && col < cols) {
-    float t = s_sum[0][c];
+// dw[k] (+)= the blocks' partial sums in a fixed order.  A workgroup takes 32 columns: 128 slices of
+// 8 lanes (4 columns each) add up every 128th row, the slices are joined in the waves, then in LDS.
+__global__ __launch_bounds__(1024) void k_norm_dweight(const float* ws, int blocks, int32_t pitch,
+                                                       int32_t cols, float* dw, int accumulate) {
+  __shared__ f4 s_sum[16][8];
+  const int q = threadIdx.x & 7, s = threadIdx.x >> 3;
+  const float* p = ws + blockIdx.x * 32 + q * 4;
+  f4 acc = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int i = s; i < blocks; i += 128) acc += *reinterpret_cast<const f4*>(p + (int64_t)i * pitch);
 #pragma unroll
-    for (int i = 1; i < 32; ++i) t += s_sum[i][c];
+  for (int d = 8; d < 64; d <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], d, 64);
+  if (lane_id() < 8) s_sum[wave_id()][q] = acc;
+  __syncthreads();
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x < 32 && col < cols) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += s_sum[i][threadIdx.x >> 2][threadIdx.x & 3];
     dw[col] = accumulate ? dw[col] + t : t;
   }
-}
-
-bool vectors(const Mat& a, int dtype) {
-  const int64_t bytes = dtype == kF32 ? 4 : 2;
-  return (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && (a.ld * bytes & 15) == 0;
 }
 
 // Calls f with the threads per row and the octets per thread as constants.  Rows of up to 2048
@@ -223,39 +300,48 @@ void by_columns(int32_t cols, F&& f) {
     f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
 }
 
-template <int DT, bool kVec, bool kRandom>
+template <int DT, bool kRandom>
 void forward(const NormArgs& a, hipStream_t st) {
   by_columns(a.cols, [&](auto tpr, auto nv) {
     constexpr int nt = block_threads<tpr>();
-    k_rmsnorm<DT, kVec, kRandom, tpr, nv>
-        <<<blocks_for(a.rows, nt / tpr), nt, 0, st>>>(a);
+    k_rmsnorm<DT, kRandom, tpr, nv><<<blocks_for(a.rows, nt / tpr), nt, 0, st>>>(a);
   });
 }
 
 template <int DT>
 void forward(const NormArgs& a, hipStream_t st) {
-  const bool vec = vectors(a.x, DT) && (!a.res.p || vectors(a.res, DT)) &&
-                   (!a.h.p || vectors(a.h, DT)) && (!a.y.p || vectors(a.y, DT));
-  if (vec)
-    a.round.random ? forward<DT, true, true>(a, st) : forward<DT, true, false>(a, st);
+  a.round.random ? forward<DT, true>(a, st) : forward<DT, false>(a, st);
+}
+
+// The backward pass's threads and octets: more columns of dw a thread than the forward pass has of
+// its row, but no more than 512 threads, which leaves them 256 registers.
+template <typename F>
+void by_columns_backward(int32_t cols, F&& f) {
+  const int octets = (cols + 7) / 8;
+  if (octets <= 64)
+    f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+  else if (octets <= 128)
+    f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+  else if (octets <= 256)
+    f(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
+  else if (octets <= 512)
+    f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+  else if (octets <= 1024)
+    f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+  else if (octets <= 1536)
+    f(std::integral_constant<int, 512>(), std::integral_constant<int, 3>());
+  else if (octets <= 2048)
+    f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
   else
-    a.round.random ? forward<DT, false, true>(a, st) : forward<DT, false, false>(a, st);
-}
-
-template <int DT, bool kVec>
-void backward(const NormGradArgs& a, hipStream_t st) {
-  const int64_t workers = norm_grad_workers(a.rows, a.cols);
-  by_columns(a.cols, [&](auto tpr, auto nv) {
-    constexpr int nt = block_threads<tpr>();
-    k_rmsnorm_backward<DT, kVec, tpr, nv>
-        <<<blocks_for(workers, nt / tpr), nt, 0, st>>>(a, workers);
-  });
+    f(std::integral_constant<int, 512>(), std::integral_constant<int, 8>());
 }
 
 template <int DT>
 void backward(const NormGradArgs& a, hipStream_t st) {
-  const bool vec = vectors(a.dy, DT) && (!a.dres.p || vectors(a.dres, DT)) && vectors(a.dx, DT);
-  vec ? backward<DT, true>(a, st) : backward<DT, false>(a, st);
+  const unsigned blocks = (unsigned)norm_grad_blocks(a.rows, a.cols);
+  by_columns_backward(a.cols, [&](auto tpr, auto nv) {
+    k_rmsnorm_backward<DT, tpr, nv><<<blocks, block_threads<tpr>(), 0, st>>>(a);
+  });
 }
 
 }  // namespace
@@ -267,9 +353,13 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-int64_t norm_grad_workers(int64_t rows, int32_t cols) {
-  (void)cols;
-  return rows < 1024 ? rows : 1024;
+// Blocks of a backward call: at least 4 rows a worker, so that the partial sums stay small beside
+// the rows, but one block a CU first; at most 1024 (four a CU).
+int64_t norm_grad_blocks(int64_t rows, int32_t cols) {
+  const int64_t per = (cols + 7) / 8 <= 256 ? 4 : 1;   // workers of a block
+  const int64_t most = (rows + per - 1) / per, want = (rows + 4 * per - 1) / (4 * per);
+  const int64_t blocks = want < 256 ? 256 : want > 1024 ? 1024 : want;
+  return blocks < most ? blocks : most;
 }
 
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t st) {
@@ -281,7 +371,7 @@ hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t st) {
   }
   if (a.dweight && !(a.rows == 0 && a.accumulate)) {
     const int32_t pitch = (a.cols + kActGroup - 1) / kActGroup * kActGroup;
-    k_norm_dweight<<<pitch / 32, 1024, 0, st>>>(a.ws, norm_grad_workers(a.rows, a.cols), pitch,
+    k_norm_dweight<<<pitch / 32, 1024, 0, st>>>(a.ws, (int)norm_grad_blocks(a.rows, a.cols), pitch,
                                                 a.cols, a.dweight, a.accumulate);
   }
   return hipGetLastError();

@@ -35,7 +35,10 @@ struct Tile {
   // 64 bytes past a row: the four rows of a transposing read start in different quarters of the banks
   static constexpr int kPitchN = TN + 32, kPitchK = TK + 32;
   static constexpr int kSlices = BM / 16;   // rows of one matrix instruction
-  static_assert(kThreads == 2 * TN && TN == TK, "a thread stages one octet of a slice");
+  // Staging: an item is one octet a thread, kRowsN rows of a step's dY or kRowsK rows of its Z.
+  static constexpr int kRowsN = kThreads / (TN / 8), kRowsK = kThreads / (TK / 8);
+  static constexpr int kItemsN = BM / kRowsN, kItemsK = BM / kRowsK;
+  static_assert(BM % kRowsN == 0 && BM % kRowsK == 0, "whole items");
 };
 
 __device__ __forceinline__ uint32_t pack_high(float a, float b) {   // their upper halves
@@ -50,40 +53,16 @@ __device__ __forceinline__ b8 fragment(const short* p, int pitch) {
   return __builtin_bit_cast(b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// 8 columns of a row as they lie in memory; a row may start at any element, which a 16-byte load
-// bears.
-template <int DT>
-struct Raw {
-  typename Elt<DT>::T v[8];
-};
-template <int DT>
-__device__ __forceinline__ Raw<DT> load_raw(const void* p) {
-  Raw<DT> r;
-  __builtin_memcpy(&r, p, sizeof r);
-  return r;
-}
-// The same where the row (in) or its columns may end: zeros past them.
-template <int DT>
-__device__ __forceinline__ Raw<DT> load_edge(const typename Elt<DT>::T* p, int col, int cols,
-                                             bool in) {
-  typedef typename Elt<DT>::T T;
-  if (in && col + 8 <= cols) return load_raw<DT>(p + col);
-  Raw<DT> r;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) r.v[j] = in && col + j < cols ? p[col + j] : (T)0.0f;
-  return r;
-}
-
 // The bf16 parts of 8 values, part q at y + q * plane.
 template <int DT>
 __device__ __forceinline__ void store_parts(short* y, int plane, const Raw<DT>& r) {
   if constexpr (DT == kBF16) {
-    *reinterpret_cast<u4*>(y) = __builtin_bit_cast(u4, r);
+    *reinterpret_cast<u4*>(y) = r.w[0];
   } else {
     float v[8];
+    to_float8<DT>(r, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = to_float(r.v[j]);
       // a NaN whose upper half alone would read as Inf
       if (DT == kF32 && v[j] != v[j]) v[j] = __uint_as_float(0x7FC00000u);
     }
@@ -119,7 +98,8 @@ __device__ __forceinline__ void tile_of(int tiles_n, int tiles_k, int* tn, int* 
 template <int DT, typename C>
 __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int splits) {
   typedef typename Elt<DT>::T T;
-  constexpr int NS = parts<DT>(), NP = C::kSlices, kPieces = NS * NP;
+  constexpr int NS = parts<DT>(), kPieces = NS * C::kSlices;
+  constexpr int NY = C::kItemsN, NZ = C::kItemsK;
   constexpr int kPlane = C::kBM * C::kPitchN, kStage = NS * kPlane + C::kBM * C::kPitchK;
   __shared__ __align__(16) short s_mem[2 * kStage];   // two stages: the parts of dY, then Z
   int tn, tk;
@@ -138,36 +118,51 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
   const int64_t whole = ld < 8 || ld > (1 << 24) || octets > (1 << 22) ? 0
                         : (wide ? a.rows : a.rows - 1) / C::kBM;
 
-  // This thread stages row r, octet c of every slice.
-  const int r = threadIdx.x / (C::kTN / 8), c = threadIdx.x % (C::kTN / 8);
-  const int my_octet = min(k0 / 8 + c, octets - 1);
-  const bool has_z = k0 / 8 + c < octets;
-  const uint32_t y_off = (uint32_t)(r * ld + min(n0 + 8 * c, a.n_out - 1)) * (uint32_t)sizeof(T);
-  const uint32_t z_off = (uint32_t)(r * octets + my_octet) * 8u;
-  const uint32_t e_off = (uint32_t)(r * groups + (my_octet >> 2));
-  Raw<DT> y[NP];
-  u2 z[NP];
-  uint32_t e[NP];
+  // This thread stages row r, octet c of every item.
+  const int ry = threadIdx.x / (C::kTN / 8), cy = threadIdx.x % (C::kTN / 8);
+  const int rz = threadIdx.x / (C::kTK / 8), cz = threadIdx.x % (C::kTK / 8);
+  const int my_octet = min(k0 / 8 + cz, octets - 1);
+  const bool has_z = k0 / 8 + cz < octets;
+  const uint32_t y_off = (uint32_t)(ry * ld + min(n0 + 8 * cy, a.n_out - 1)) * (uint32_t)sizeof(T);
+  const uint32_t z_off = (uint32_t)(rz * octets + my_octet) * 8u;
+  const uint32_t e_off = (uint32_t)(rz * groups + (my_octet >> 2));
+  Raw<DT> y[NY];
+  u2 z[NZ];
+  uint32_t e[NZ];
+  // Loads item p of a step: dY's first, then Z's.  The rows' base is the same in all lanes.
   auto load_whole = [&](int64_t step, int p) {
-    const int64_t m = step * C::kBM + 16 * p;   // the same in all lanes
-    y[p] = load_raw<DT>(static_cast<const char*>(a.dy.p) + m * ld * (int64_t)sizeof(T) + y_off);
-    z[p] = *reinterpret_cast<const u2*>(reinterpret_cast<const char*>(a.codes) + m * octets * 8 + z_off);
-    e[p] = (a.exps + m * groups)[e_off];
+    if (p < NY) {
+      const int64_t m = step * C::kBM + C::kRowsN * p;
+      y[p] = load_raw<DT>(static_cast<const char*>(a.dy.p) + m * ld * (int64_t)sizeof(T) + y_off);
+    } else {
+      const int64_t m = step * C::kBM + C::kRowsK * (p - NY);
+      z[p - NY] = *reinterpret_cast<const u2*>(reinterpret_cast<const char*>(a.codes) +
+                                               m * octets * 8 + z_off);
+      e[p - NY] = (a.exps + m * groups)[e_off];
+    }
   };
   auto load_any_rows = [&](int64_t step, int p) {
-    const int64_t m = step * C::kBM + 16 * p + r;
-    const bool in = m < a.rows;
-    y[p] = load_edge<DT>(static_cast<const T*>(a.dy.p) + m * ld, n0 + 8 * c, a.n_out, in);
-    z[p] = u2{0, 0};
-    e[p] = 0;
-    if (in && has_z) {
-      const int64_t i = m * octets + k0 / 8 + c;
-      z[p] = reinterpret_cast<const u2*>(a.codes)[i];
-      e[p] = a.exps[i >> 2];
+    if (p < NY) {
+      const int64_t m = step * C::kBM + C::kRowsN * p + ry;
+      y[p] = load_raw<DT>(static_cast<const T*>(a.dy.p) + m * ld, n0 + 8 * cy,
+                          m < a.rows ? a.n_out : 0);
+    } else {
+      const int64_t m = step * C::kBM + C::kRowsK * (p - NY) + rz;
+      z[p - NY] = u2{0, 0};
+      e[p - NY] = 0;
+      if (m < a.rows && has_z) {
+        const int64_t i = m * octets + k0 / 8 + cz;
+        z[p - NY] = reinterpret_cast<const u2*>(a.codes)[i];
+        e[p - NY] = a.exps[i >> 2];
+      }
     }
   };
   auto store = [&](short* stage, int p) {
-    store_parts<DT>(stage + (16 * p + r) * C::kPitchN + 8 * c, kPlane, y[p]);
+    if (p < NY) {
+      store_parts<DT>(stage + (C::kRowsN * p + ry) * C::kPitchN + 8 * cy, kPlane, y[p]);
+      return;
+    }
+    p -= NY;
     // u = code + 128 is a byte, which one instruction makes a float; u * scale - 128 * scale is the
     // restored value without a rounding (and NaN for a bad group: Inf - Inf)
     const float scale = exponent_scale(e[p]), shift = -128.0f * scale;
@@ -181,7 +176,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
       w[2 * h] = pack_high(v[0], v[1]);
       w[2 * h + 1] = pack_high(v[2], v[3]);
     }
-    *reinterpret_cast<u4*>(stage + NS * kPlane + (16 * p + r) * C::kPitchK + 8 * c) = w;
+    *reinterpret_cast<u4*>(stage + NS * kPlane + (C::kRowsK * p + rz) * C::kPitchK + 8 * cz) = w;
   };
   // The lane's place in a transposing read.
   const int fr = 8 * (lane >> 5) + ((lane & 15) >> 2), fc = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
@@ -221,8 +216,8 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
         }
       }
 #pragma unroll
-      for (int t = 0; t < NP; ++t)
-        if (t * (kPieces - 1) / NP == i) {
+      for (int t = 0; t < NY + NZ; ++t)
+        if (t * (kPieces - 1) / (NY + NZ) == i) {
           if (more1) store(nxt, t);
           if (all)
             load_whole(s + 2, t);
@@ -246,17 +241,19 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
   };
   if (first < last) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) load_any_rows(first, p);
+    for (int p = 0; p < NY + NZ; ++p) load_any_rows(first, p);
 #pragma unroll
-    for (int p = 0; p < NP; ++p) store(cur, p);
+    for (int p = 0; p < NY + NZ; ++p) store(cur, p);
     if (first + 1 < last)
 #pragma unroll
-      for (int p = 0; p < NP; ++p) load_any_rows(first + 1, p);
+      for (int p = 0; p < NY + NZ; ++p) load_any_rows(first + 1, p);
     __syncthreads();
     read_z(cur, 0, fz);
     read_y(cur, 0, 0, fy);
     const int64_t lim = whole < last ? whole : last;
     int64_t s = first;
+    // nothing in flight: the loop's own waits then count its own loads only, in their order
+    __builtin_amdgcn_s_waitcnt(0x0F70);
     for (; s + 2 < lim; ++s) step(s, std::true_type());
     for (; s < last; ++s) step(s, std::false_type());
   }

@@ -91,7 +91,7 @@ def backward(dy=A, ld_dy=64, dtype=1, rows=4, cols=64, codes=B, exps=C, rstd=D, 
 @pytest.mark.parametrize("case,want", [
     (dict(dtype=3), BAD), (dict(wd=3), BAD), (dict(dy=None), BAD), (dict(dx=None), BAD),
     (dict(codes=None), BAD), (dict(exps=None), BAD), (dict(rstd=None), BAD), (dict(ws=None), BAD),
-    (dict(n=4 * 64 * 4 - 1), BAD), (dict(ws=H + (1 << 20) + 8), BAD), (dict(dw=H + 2), BAD),
+    (dict(n=gca.rmsnorm_backward_workspace(4, 64) - 1), BAD), (dict(ws=H + (1 << 20) + 8), BAD), (dict(dw=H + 2), BAD),
     (dict(ld_dx=63), BAD), (dict(dx=B), BAD), (dict(dx=A + 2), BAD), (dict(dx=F, ld_dx=128), BAD),
     (dict(dw=G), BAD), (dict(ws=A), BAD), (dict(ws=H), BAD), (dict(dw=D), BAD),
     (dict(cols=32769), UNSUPPORTED), (dict(rows=-1), BAD),
