@@ -56,19 +56,51 @@ __device__ __forceinline__ Raw<DT> load_raw(const void* p) {
   __builtin_memcpy(&r, p, sizeof r);
   return r;
 }
-// 8 columns from col of the row at p, zeros from `cols` on.
+// Moves the words down by n halves of a word (n < 2 N), zeros from the top.
+template <int N>
+__device__ __forceinline__ void shift_down(uint32_t (&d)[N], uint32_t n) {
+#pragma unroll
+  for (int q = N / 2; q >= 1; q >>= 1)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t from = j + q < N ? d[j + q] : 0u;
+      d[j] = n & (2 * q) ? from : d[j];
+    }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t next = j + 1 < N ? d[j + 1] : 0u;
+    d[j] = n & 1 ? (d[j] >> 16) | (next << 16) : d[j];
+  }
+}
+
+// 8 columns from col of the row at p, zeros from `cols` on.  Where the row ends inside the octet its
+// last 8 columns are loaded and moved into place: one load, as everywhere else.
 template <int DT>
 __device__ __forceinline__ Raw<DT> load_raw(const typename Elt<DT>::T* p, int col, int cols) {
+  constexpr int kWords = 4 * Raw<DT>::kWords, kHalves = sizeof(typename Elt<DT>::T) / 2;
   if (col + 8 <= cols) return load_raw<DT>(p + col);
   Raw<DT> r = {};
+  if (col >= cols) return r;
+  uint32_t d[kWords] = {};
+  if (cols >= 8) {
+    __builtin_memcpy(d, p + cols - 8, sizeof d);
+    shift_down<kWords>(d, (uint32_t)(col + 8 - cols) * kHalves);
+  } else {   // a row of fewer than 8 columns: from its end, each column under the last
+#pragma unroll 1
+    for (int j = cols - 1; j >= 0; --j) {
+      uint32_t e;
+      if constexpr (kHalves == 1)
+        e = __builtin_bit_cast(uint16_t, p[j]);
+      else
+        e = __builtin_bit_cast(uint32_t, p[j]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (col + j >= cols) continue;
-    if constexpr (sizeof(typename Elt<DT>::T) == 2)
-      r.w[0][j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[col + j]) << (16 * (j % 2));
-    else
-      r.w[j / 4][j % 4] = __builtin_bit_cast(uint32_t, p[col + j]);
+      for (int i = kWords - 1; i >= 0; --i) {
+        const uint32_t below = i ? d[i - 1] : (kHalves == 1 ? e << 16 : e);
+        d[i] = kHalves == 1 ? (d[i] << 16) | (below >> 16) : below;
+      }
+    }
   }
+  __builtin_memcpy(&r, d, sizeof r);
   return r;
 }
 template <int DT>
@@ -199,14 +231,48 @@ __device__ __forceinline__ u2 encode8(const float (&v)[8], uint64_t block, uint3
   return e == kExpBad ? u2{0, 0} : r;
 }
 
-// code * scale for 8 codes: exact (7 bits and a sign times a power of two); 0 * Inf is the NaN
-// of a bad group.
+// code * scale for 8 codes, exact (7 bits and a sign times a power of two).  u = code + 128 is a byte,
+// which one instruction makes a float, and u * scale - 128 * scale rounds nothing; for a bad group
+// it is Inf - Inf, the NaN that it stands for.
 __device__ __forceinline__ void decode8(u2 c, float scale, float (&v)[8]) {
+  const float shift = -128.0f * scale;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u = c[h] ^ 0x80808080u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[4 * h + j] = (float)(int8_t)(c[h] >> (8 * j)) * scale;
+    for (int j = 0; j < 4; ++j) v[4 * h + j] = fmaf((float)((u >> (8 * j)) & 0xFFu), scale, shift);
+  }
+}
+
+// A value from another lane of the row of 16 (DPP control word), for 4- and 8-byte types.
+template <int kCtrl, typename S>
+__device__ __forceinline__ S from_lane(S v) {
+  int w[sizeof(S) / 4];
+  __builtin_memcpy(w, &v, sizeof v);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(S) / 4); ++i)
+    w[i] = __builtin_amdgcn_mov_dpp(w[i], kCtrl, 0xF, 0xF, true);
+  __builtin_memcpy(&v, w, sizeof v);
+  return v;
+}
+template <typename S>
+__device__ __forceinline__ S read_lane(S v, int lane) {
+  int w[sizeof(S) / 4];
+  __builtin_memcpy(w, &v, sizeof v);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(S) / 4); ++i) w[i] = __builtin_amdgcn_readlane(w[i], lane);
+  __builtin_memcpy(&v, w, sizeof v);
+  return v;
+}
+// Sum over the wave's 64 lanes, all active, in a fixed order: neighbours, pairs, halves of a row
+// of 16, its two halves, then the four rows.
+template <typename S>
+__device__ __forceinline__ S wave_sum(S v) {
+  v += from_lane<0xB1>(v);    // lane ^ 1
+  v += from_lane<0x4E>(v);    // lane ^ 2
+  v += from_lane<0x141>(v);   // mirrored in the half row
+  v += from_lane<0x140>(v);   // mirrored in the row
+  return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
 }
 
 // How the writers and readers of whole rows spread octets over waves: a row has `octets`

@@ -22,8 +22,7 @@ namespace {
 // every one of them.  The order is fixed.
 template <int TPR, typename S>
 __device__ __forceinline__ S row_sum(S v, S* s_part) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  v = wave_sum(v);
   if (TPR == 64) return v;
   if (lane_id() == 0) s_part[wave_id()] = v;
   __syncthreads();
@@ -33,6 +32,9 @@ __device__ __forceinline__ S row_sum(S v, S* s_part) {
   __syncthreads();
   return t;
 }
+
+// This thread's wave, known to be the same in the whole wave: row addresses then stay in scalar registers.
+__device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirstlane(wave_id()); }
 
 // Threads of a block: rows of up to 64 * NV octets take one wave each, four to a block.
 template <int TPR>
@@ -46,7 +48,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm(NormArgs a) {
   __shared__ double s_part[16];
   constexpr int kRows = block_threads<TPR>() / TPR;
   const int t = TPR == 64 ? lane_id() : threadIdx.x;
-  const int64_t row = (int64_t)blockIdx.x * kRows + (TPR == 64 ? wave_id() : 0);
+  const int64_t row = (int64_t)blockIdx.x * kRows + (TPR == 64 ? uniform_wave() : 0);
   if (row >= a.rows) return;   // a whole wave (TPR 64) or nobody
   const int cols = a.cols, octets = (cols + kActGroup - 1) / kActGroup * (kActGroup / 8);
   const T* x = static_cast<const T*>(a.x.p) + row * a.x.ld;
@@ -112,6 +114,13 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm(NormArgs a) {
   }
 }
 
+// Waves of a SIMD that the backward pass's registers are held to: two blocks of 512 threads a CU as
+// long as that costs no more than a few spilled registers.
+template <int TPR, int NV>
+constexpr int backward_waves() {
+  return TPR == 512 && NV <= 3 ? 4 : 1;
+}
+
 // What a thread holds of one row of the backward pass, as it lies in memory.
 template <int DT, int NV>
 struct GradRow {
@@ -127,7 +136,7 @@ struct GradRow {
 // octets a thread).  A row is held as it was loaded and expanded twice: its floats would cost half
 // of the waves.
 template <int DT, int TPR, int NV>
-__global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormGradArgs a) {
+__global__ __launch_bounds__(block_threads<TPR>(), (backward_waves<TPR, NV>())) void k_rmsnorm_backward(NormGradArgs a) {
   typedef typename Elt<DT>::T T;
   constexpr int kRows = block_threads<TPR>() / TPR, kWavesN = TPR / 64;
   constexpr bool kAhead = NV <= 2, kKeepW = NV <= 4;
@@ -135,7 +144,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormG
   __shared__ float s_dw[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * NV * 8 : 1];
   const int t = TPR == 64 ? lane_id() : threadIdx.x;
   const int64_t workers = (int64_t)gridDim.x * kRows;
-  const int64_t worker = (int64_t)blockIdx.x * kRows + (TPR == 64 ? wave_id() : 0);
+  const int64_t worker = (int64_t)blockIdx.x * kRows + (TPR == 64 ? uniform_wave() : 0);
   const int cols = a.cols, octets = (cols + kActGroup - 1) / kActGroup * (kActGroup / 8);
   const bool has_res = a.dres.p != nullptr;
 
@@ -150,6 +159,8 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormG
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int octet = t + v * TPR, col = octet * 8;
+      // past the row's end dy is 0, so whatever the codes are there adds nothing (a bad last group
+      // makes the row NaN by its own columns)
       r.dy[v] = load_raw<DT>(dy, col, cols);
       if (has_res) r.dres[v] = load_raw<DT>(dres, col, cols);
       r.codes[v] = u2{0, 0};
@@ -162,17 +173,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormG
     }
     r.rstd = a.rstd[row];
   };
-  // z of octet v; the padding of the last octets is not part of the row, whatever its group
-  // restores to
-  auto restored = [&](const GradRow<DT, NV>& r, int v, float (&z)[8]) {
-    decode8(r.codes[v], exponent_scale(r.exps[v]), z);
-    const int col = (t + v * TPR) * 8;
-    if (col + 8 > cols)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = col + j < cols ? z[j] : 0.0f;
-  };
-
-  GradRow<DT, NV> cur, nxt;
+  GradRow<DT, NV> cur = {}, nxt = {};   // no dres: zeros are added
   int turn = 0;
   if (worker < a.rows) load(worker, cur);
   for (int64_t row = worker; row < a.rows; row += workers) {
@@ -183,17 +184,17 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormG
     for (int v = 0; v < NV; ++v) {
       float g[8], z[8];
       to_float8<DT>(cur.dy[v], g);
-      restored(cur, v, z);
+      decode8(cur.codes[v], exponent_scale(cur.exps[v]), z);
       if (!kKeepW) load8_any(a.weight, a.weight_dtype, (t + v * TPR) * 8, cols, w[0]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[v][j] = fmaf(g[j], z[j], dw[v][j]);
+        asm("" : "+v"(dw[v][j]));   // now, or g and z are kept for it until the row's end
         s = fmaf(g[j] * w[kKeepW ? v : 0][j], z[j], s);
       }
     }
     // the waves' sums alternate between two places, so that one meeting a row is enough
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
+    s = wave_sum(s);
     if (kWavesN > 1) {
       if (lane_id() == 0) s_part[turn][wave_id()] = s;
       __syncthreads();
@@ -216,13 +217,12 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm_backward(NormG
       const int col = (t + v * TPR) * 8;
       float g[8], z[8], r[8];
       to_float8<DT>(cur.dy[v], g);
-      restored(cur, v, z);
+      decode8(cur.codes[v], exponent_scale(cur.exps[v]), z);
       if (!kKeepW) load8_any(a.weight, a.weight_dtype, col, cols, w[0]);
-      if (has_res) to_float8<DT>(cur.dres[v], r);
+      to_float8<DT>(cur.dres[v], r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = cur.rstd * fmaf(-z[j], c, g[j] * w[kKeepW ? v : 0][j]);
-        g[j] = has_res ? d + r[j] : d;
+        g[j] = cur.rstd * fmaf(-z[j], c, g[j] * w[kKeepW ? v : 0][j]) + r[j];
       }
       store8<DT>(dx, col, cols, g);
     }
@@ -313,8 +313,8 @@ void forward(const NormArgs& a, hipStream_t st) {
   a.round.random ? forward<DT, true>(a, st) : forward<DT, false>(a, st);
 }
 
-// The backward pass's threads and octets: more columns of dw a thread than the forward pass has of
-// its row, but no more than 512 threads, which leaves them 256 registers.
+// The backward pass's threads and octets: 512 threads as long as they do, which leaves a thread
+// twice the registers of 1024.
 template <typename F>
 void by_columns_backward(int32_t cols, F&& f) {
   const int octets = (cols + 7) / 8;
@@ -333,7 +333,7 @@ void by_columns_backward(int32_t cols, F&& f) {
   else if (octets <= 2048)
     f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
   else
-    f(std::integral_constant<int, 512>(), std::integral_constant<int, 8>());
+    f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
 }
 
 template <int DT>
@@ -354,12 +354,16 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
 }
 
 // Blocks of a backward call: at least 4 rows a worker, so that the partial sums stay small beside
-// the rows, but one block a CU first; at most 1024 (four a CU).
+// the rows, but one block a CU first; at most 1024 threads a CU.
 int64_t norm_grad_blocks(int64_t rows, int32_t cols) {
-  const int64_t per = (cols + 7) / 8 <= 256 ? 4 : 1;   // workers of a block
-  const int64_t most = (rows + per - 1) / per, want = (rows + 4 * per - 1) / (4 * per);
-  const int64_t blocks = want < 256 ? 256 : want > 1024 ? 1024 : want;
-  return blocks < most ? blocks : most;
+  int64_t per = 1, most = 256;
+  by_columns_backward(cols, [&](auto tpr, auto) {
+    per = block_threads<tpr>() / tpr;   // workers of a block
+    most = 256 * 1024 / block_threads<tpr>();
+  });
+  const int64_t need = (rows + per - 1) / per, want = (rows + 4 * per - 1) / (4 * per);
+  const int64_t blocks = want < 256 ? 256 : want > most ? most : want;
+  return blocks < need ? blocks : need;
 }
 
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t st) {

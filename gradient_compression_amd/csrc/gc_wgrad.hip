@@ -163,19 +163,11 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
       return;
     }
     p -= NY;
-    // u = code + 128 is a byte, which one instruction makes a float; u * scale - 128 * scale is the
-    // restored value without a rounding (and NaN for a bad group: Inf - Inf)
-    const float scale = exponent_scale(e[p]), shift = -128.0f * scale;
+    float v[8];
+    decode8(z[p], exponent_scale(e[p]), v);
     u4 w;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t u = z[p][h] ^ 0x80808080u;
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = fmaf((float)((u >> (8 * j)) & 0xFFu), scale, shift);
-      w[2 * h] = pack_high(v[0], v[1]);
-      w[2 * h + 1] = pack_high(v[2], v[3]);
-    }
+    for (int j = 0; j < 4; ++j) w[j] = pack_high(v[2 * j], v[2 * j + 1]);
     *reinterpret_cast<u4*>(stage + NS * kPlane + (C::kRowsK * p + rz) * C::kPitchK + 8 * cz) = w;
   };
   // The lane's place in a transposing read.
