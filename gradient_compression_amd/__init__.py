@@ -8,6 +8,7 @@ for device memory and streams.  The package fails loudly when the library is mis
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -490,8 +491,27 @@ def read_f32(x, sink, stream=None):
 
 
 # ------------------------------------------------------------ activation checkpoints (8 bits)
+# These calls are small beside a training step's but many, so their checks take the shortest way:
+# torch's names and the type codes are looked up once, pointers go to ctypes as integers.
 ACT_GROUP = 32        # columns that share a scale
-_GC_DTYPES = {"float32": 0, "bfloat16": 1, "float16": 2}
+_types = None         # (torch, Tensor, {dtype: code}, current stream's handle) at the first call
+
+
+def _load_types():
+    global _types
+    import torch
+    # the current stream as an integer, where this torch can tell it without a Stream object
+    handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _types = (torch, torch.Tensor,
+              {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, handle)
+    return _types
+
+
+def _current_device():
+    torch = (_types or _load_types())[0]
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or \
+        torch.cuda.is_available() else -2
 
 
 def act_layout(cols: int):
@@ -503,92 +523,96 @@ def act_layout(cols: int):
     return pitch.value, groups.value
 
 
-def _dtype_code(t, name):
-    if t is None:
-        raise TypeError(f"{name} must be a torch tensor")
-    code = _GC_DTYPES.get(str(t.dtype).rpartition(".")[2])
-    if code is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return code
-
-
-def _on_device(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor):
+def _refuse_place(t, name, dev):
+    if not isinstance(t, _types[1]):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must live on the GPU")
-    cur = torch.cuda.current_device()
-    if t.device.index != cur:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _matrix(t, name, like=None, like_name=""):
-    """(pointer, row pitch, rows, columns) of a tensor whose last dimension is the columns (unit
-    stride) and whose other dimensions are evenly spaced rows; with ``like``, of its shape and
-    type.  None -> a NULL matrix."""
-    if t is None:
-        return None, 0, 0, 0
-    _on_device(t, name)
+def _matrix(t, name, dev):
+    """(pointer, row pitch, rows, columns, type code) of a tensor whose last dimension is the
+    columns (unit stride) and whose other dimensions are evenly spaced rows."""
+    if not isinstance(t, _types[1]) or t.get_device() != dev:
+        _refuse_place(t, name, dev)
+    code = _types[2].get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if t.dim() < 1:
         raise ValueError(f"{name} needs a dimension of columns")
-    cols = t.shape[-1]
-    rows = 1
-    for n in t.shape[:-1]:
-        rows *= n
-    if cols == 0 or rows == 0:
-        m = (None, 0, rows, cols)
-    else:
-        if cols > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name} must have unit stride along its last dimension")
-        lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
-        for (_, outer), (n, inner) in zip(lead, lead[1:]):
-            if outer != n * inner:
-                raise ValueError(f"{name} must have evenly spaced rows")
-        ld = lead[-1][1] if lead else cols
-        if ld < cols:
-            raise ValueError(f"{name} has overlapping rows")
-        m = (ctypes.c_void_p(t.data_ptr()), ld, rows, cols)
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
-        if tuple(t.shape) != tuple(like.shape):
-            raise ValueError(f"{name} must have the shape of {like_name}, {tuple(like.shape)}, "
-                             f"got {tuple(t.shape)}")
-    return m
+    cols, numel = t.size(-1), t.numel()
+    if numel == 0:
+        rows = 1
+        for n in t.shape[:-1]:
+            rows *= n
+        return None, 0, rows, cols, code
+    rows = numel // cols
+    if t.is_contiguous():
+        return t.data_ptr(), cols, rows, cols, code
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    for (_, outer), (n, inner) in zip(lead, lead[1:]):
+        if outer != n * inner:
+            raise ValueError(f"{name} must have evenly spaced rows")
+    ld = lead[-1][1] if lead else cols
+    if ld < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.data_ptr(), ld, rows, cols, code
 
 
-def _checkpoint(codes, exps, rows, cols):
-    """Device pointers of the two arrays of a rows x cols checkpoint."""
-    import torch
-    pitch, groups = act_layout(cols)
-    out = []
-    for t, dtype, name, width in ((codes, torch.int8, "codes", pitch),
-                                  (exps, torch.uint8, "exps", groups)):
-        out.append(_dev_ptr(t, dtype, name))
-        if t is not None and t.numel() != rows * width:
-            raise ValueError(f"{name} must hold {rows} x {width} elements, has {t.numel()}")
-    return out
-
-
-def _vector(t, name, cols):
-    """(pointer, type code) of a vector over the columns; NULL for None."""
+def _like(t, name, dev, like, like_name):
+    """(pointer, row pitch) of a matrix of the shape and type of another; NULL for None."""
     if t is None:
         return None, 0
-    code = _dtype_code(t, name)
-    p = _dev_ptr(t, t.dtype, name)
-    if t.numel() != cols:
-        raise ValueError(f"{name} must have {cols} elements, has {t.numel()}")
-    return p, code
+    p, ld, _, _, _ = _matrix(t, name, dev)
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have the shape of {like_name}, {tuple(like.shape)}, got "
+                         f"{tuple(t.shape)}")
+    return p, ld
 
 
-def _rounding(stochastic, seed, step):
-    return int(bool(stochastic)), int(seed) & (2 ** 64 - 1), int(step) & (2 ** 64 - 1)
+def _array(t, name, dtype, numel, dev):
+    """Pointer of a contiguous tensor of exactly numel elements; NULL for None."""
+    if t is None:
+        return None
+    if not isinstance(t, _types[1]) or t.get_device() != dev:
+        _refuse_place(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} elements, has {t.numel()}")
+    return t.data_ptr() if numel else None
 
 
-def _workspace(workspace, need, stream):
+def _checkpoint(codes, exps, rows, cols, dev):
+    """Pointers of the two arrays of a rows x cols checkpoint."""
+    torch = _types[0]
+    groups = -(-cols // ACT_GROUP)
+    return (_array(codes, "codes", torch.int8, rows * groups * ACT_GROUP, dev),
+            _array(exps, "exps", torch.uint8, rows * groups, dev))
+
+
+def _columns(t, name, cols, dev):
+    """(pointer, type code) of a vector over the columns, of any of the types; NULL for None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, _types[1]):
+        _refuse_place(t, name, dev)
+    code = _types[2].get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _array(t, name, t.dtype, cols, dev), code
+
+
+def _workspace(workspace, need, stream, dev):
     """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one on the stream."""
-    import torch
+    torch = _types[0]
     if workspace is None:
         if need == 0:
             return None, 0, None
@@ -597,27 +621,37 @@ def _workspace(workspace, need, stream):
         else:
             with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
-    p = _dev_ptr(workspace, workspace.dtype, "workspace")
-    return p, workspace.numel() * workspace.element_size(), workspace
+    elif not isinstance(workspace, _types[1]) or workspace.get_device() != dev:
+        _refuse_place(workspace, "workspace", dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _raw_stream(stream, dev):
+    return _types[3](dev) if stream is None else stream.cuda_stream
+
+
+_MASK64 = 2 ** 64 - 1
 
 
 def act_quant(x, codes, exps, stochastic: bool = False, seed: int = 0, step: int = 0,
               stream=None):
     """x into its 8-bit checkpoint: one power-of-two scale for 32 columns of a row, codes rounded
     to nearest even or, with ``stochastic``, by the Philox stream of (seed, step)."""
-    p, ld, rows, cols = _matrix(x, "x")
-    code = _dtype_code(x, "x")
-    cp, ep = _checkpoint(codes, exps, rows, cols)
-    _check(lib().gc_act_quant(p, ld, code, rows, cols, *_rounding(stochastic, seed, step), cp, ep,
-                              _stream(stream)), "gc_act_quant")
+    dev = _current_device()
+    p, ld, rows, cols, code = _matrix(x, "x", dev)
+    cp, ep = _checkpoint(codes, exps, rows, cols, dev)
+    _check(lib().gc_act_quant(p, ld, code, rows, cols, 1 if stochastic else 0, int(seed) & _MASK64,
+                              int(step) & _MASK64, cp, ep, _raw_stream(stream, dev)), "gc_act_quant")
 
 
 def act_restore(codes, exps, out, stream=None):
     """out = the checkpoint's values, rounded to out's type (exact in float32 and bfloat16)."""
-    p, ld, rows, cols = _matrix(out, "out")
-    code = _dtype_code(out, "out")
-    cp, ep = _checkpoint(codes, exps, rows, cols)
-    _check(lib().gc_act_restore(cp, ep, rows, cols, p, ld, code, _stream(stream)),
+    dev = _current_device()
+    p, ld, rows, cols, code = _matrix(out, "out", dev)
+    cp, ep = _checkpoint(codes, exps, rows, cols, dev)
+    _check(lib().gc_act_restore(cp, ep, rows, cols, p, ld, code, _raw_stream(stream, dev)),
            "gc_act_restore")
 
 
@@ -628,23 +662,24 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, h=None, y=None, rs
     8-bit checkpoint into (codes, exps).  ``h``, ``y``, ``rstd`` (float32[rows]) and the
     checkpoint are written where given (at least y or the checkpoint); h or y may be x or
     residual itself."""
-    import torch
-    xp, ld_x, rows, cols = _matrix(x, "x")
-    code = _dtype_code(x, "x")
-    rp, ld_r, _, _ = _matrix(residual, "residual", x, "x")
-    hp, ld_h, _, _ = _matrix(h, "h", x, "x")
-    yp, ld_y, _, _ = _matrix(y, "y", x, "x")
-    wp, wcode = _vector(weight, "weight", cols)
+    dev = _current_device()
+    xp, ld_x, rows, cols, code = _matrix(x, "x", dev)
+    rp, ld_r = _like(residual, "residual", dev, x, "x")
+    hp, ld_h = _like(h, "h", dev, x, "x")
+    yp, ld_y = _like(y, "y", dev, x, "x")
+    wp, wcode = _columns(weight, "weight", cols, dev)
     cp = ep = None
     if codes is not None or exps is not None:
         if codes is None or exps is None:
             raise ValueError("codes and exps go together")
-        cp, ep = _checkpoint(codes, exps, rows, cols)
-    _check(lib().gc_rmsnorm(xp, ld_x, rp, ld_r, code, rows, cols, wp, wcode, float(eps), hp, ld_h,
-                            yp, ld_y, _dev_ptr(rstd, torch.float32, "rstd", rows), cp, ep,
-                            *_rounding(stochastic, seed, step), _stream(stream)), "gc_rmsnorm")
+        cp, ep = _checkpoint(codes, exps, rows, cols, dev)
+    _check(lib().gc_rmsnorm(xp, ld_x, rp, ld_r, code, rows, cols, wp, wcode, eps, hp, ld_h, yp,
+                            ld_y, _array(rstd, "rstd", _types[0].float32, rows, dev), cp, ep,
+                            1 if stochastic else 0, int(seed) & _MASK64, int(step) & _MASK64,
+                            _raw_stream(stream, dev)), "gc_rmsnorm")
 
 
+@functools.lru_cache(maxsize=4096)
 def rmsnorm_backward_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace of a rmsnorm_backward call with dweight (host-only)."""
     n = ctypes.c_int64()
@@ -659,31 +694,28 @@ def rmsnorm_backward(dy, codes, exps, rstd, dx, weight=None, dres=None, dweight=
     t = dy * weight; dweight (float32, a segment of the flat gradient) = sum over rows of dy * z,
     added to what it holds with ``accumulate``.  dx may be dy or dres itself.  ``workspace``: a
     tensor of rmsnorm_backward_workspace bytes; allocated for the call when None."""
-    import torch
-    p, ld, rows, cols = _matrix(dy, "dy")
-    code = _dtype_code(dy, "dy")
-    xp, ld_x, _, _ = _matrix(dx, "dx", dy, "dy")
+    dev = _current_device()
+    p, ld, rows, cols, code = _matrix(dy, "dy", dev)
     if dx is None:
         raise TypeError("dx must be a torch tensor")
-    rp, ld_r, _, _ = _matrix(dres, "dres", dy, "dy")
-    cp, ep = _checkpoint(codes, exps, rows, cols)
-    wp, wcode = _vector(weight, "weight", cols)
-    dwp = _dev_ptr(dweight, torch.float32, "dweight")
-    need = 0
-    if dweight is not None:
-        if dweight.numel() != cols:
-            raise ValueError(f"dweight must have {cols} elements, has {dweight.numel()}")
-        need = rmsnorm_backward_workspace(rows, cols)
-    ws, ws_bytes, _keep = _workspace(workspace, need, stream)
+    xp, ld_x = _like(dx, "dx", dev, dy, "dy")
+    rp, ld_r = _like(dres, "dres", dev, dy, "dy")
+    cp, ep = _checkpoint(codes, exps, rows, cols, dev)
+    wp, wcode = _columns(weight, "weight", cols, dev)
+    f32 = _types[0].float32
+    dwp = _array(dweight, "dweight", f32, cols, dev)
+    need = rmsnorm_backward_workspace(rows, cols) if dweight is not None else 0
+    ws, ws_bytes, _keep = _workspace(workspace, need, stream, dev)
     _check(lib().gc_rmsnorm_backward(p, ld, code, rows, cols, cp, ep,
-                                     _dev_ptr(rstd, torch.float32, "rstd", rows), wp, wcode, rp,
-                                     ld_r, xp, ld_x, dwp, int(bool(accumulate)), ws, ws_bytes,
-                                     _stream(stream)), "gc_rmsnorm_backward")
+                                     _array(rstd, "rstd", f32, rows, dev), wp, wcode, rp, ld_r, xp,
+                                     ld_x, dwp, 1 if accumulate else 0, ws, ws_bytes,
+                                     _raw_stream(stream, dev)), "gc_rmsnorm_backward")
 
 
+@functools.lru_cache(maxsize=4096)
 def act_weight_grad_workspace(rows: int, n_out: int, cols: int, dtype) -> int:
     """Bytes of workspace of an act_weight_grad call (host-only); ``dtype``: dy's."""
-    code = _GC_DTYPES.get(str(dtype).rpartition(".")[2], -1)
+    code = (_types or _load_types())[2].get(dtype, -1)
     n = ctypes.c_int64()
     _check(lib().gc_act_weight_grad_workspace(int(rows), int(n_out), int(cols), code,
                                               ctypes.byref(n)), "gc_act_weight_grad_workspace")
@@ -697,21 +729,20 @@ def act_weight_grad(dy, codes, exps, dweight, col_scale=None, accumulate: bool =
     cols], a segment of the flat gradient viewed so) is added to with ``accumulate``.
     ``workspace``: a tensor of act_weight_grad_workspace bytes; allocated for the call when
     None."""
-    import torch
-    p, ld, rows, n_out = _matrix(dy, "dy")
-    code = _dtype_code(dy, "dy")
-    dwp = _dev_ptr(dweight, torch.float32, "dweight")
-    if dweight is None:
+    dev = _current_device()
+    p, ld, rows, n_out, code = _matrix(dy, "dy", dev)
+    if not isinstance(dweight, _types[1]):
         raise TypeError("dweight must be a torch tensor")
-    if dweight.dim() != 2 or dweight.shape[0] != n_out:
+    if dweight.dim() != 2 or dweight.size(0) != n_out:
         raise ValueError(f"dweight must be {n_out} x columns, got {tuple(dweight.shape)}")
-    cols = dweight.shape[1]
-    cp, ep = _checkpoint(codes, exps, rows, cols)
-    sp, scode = _vector(col_scale, "col_scale", cols)
-    need = act_weight_grad_workspace(rows, n_out, cols, dy.dtype)
-    ws, ws_bytes, _keep = _workspace(workspace, need, stream)
+    cols = dweight.size(1)
+    dwp = _array(dweight, "dweight", _types[0].float32, n_out * cols, dev)
+    cp, ep = _checkpoint(codes, exps, rows, cols, dev)
+    sp, scode = _columns(col_scale, "col_scale", cols, dev)
+    ws, ws_bytes, _keep = _workspace(
+        workspace, act_weight_grad_workspace(rows, n_out, cols, dy.dtype), stream, dev)
     _check(lib().gc_act_weight_grad(p, ld, code, rows, n_out, cols, cp, ep, sp, scode, dwp,
-                                    int(bool(accumulate)), ws, ws_bytes, _stream(stream)),
+                                    1 if accumulate else 0, ws, ws_bytes, _raw_stream(stream, dev)),
            "gc_act_weight_grad")
 
 
