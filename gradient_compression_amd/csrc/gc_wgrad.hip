@@ -111,8 +111,8 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
   const int64_t ld = a.dy.ld;
   const int64_t steps = (a.rows + C::kBM - 1) / C::kBM;
   const int64_t first = steps * blockIdx.y / splits, last = steps * (blockIdx.y + 1) / splits;
-  // Steps whose rows are all there and whose 16-byte loads stay inside dY whatever their column: a
-  // load that starts in a row before the last one ends before the matrix does.  The lanes of
+  // Whole steps: their rows are all there and their 16-byte loads stay inside dY whatever the column,
+  // as a load that starts in a row before the last one ends before the matrix does.  The lanes of
   // columns past n_out or the pitch read some other column there; what they add up is not stored.
   const bool wide = n0 + C::kTN <= a.n_out;
   const int64_t whole = ld < 8 || ld > (1 << 24) || octets > (1 << 22) ? 0
@@ -122,7 +122,6 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
   const int ry = threadIdx.x / (C::kTN / 8), cy = threadIdx.x % (C::kTN / 8);
   const int rz = threadIdx.x / (C::kTK / 8), cz = threadIdx.x % (C::kTK / 8);
   const int my_octet = min(k0 / 8 + cz, octets - 1);
-  const bool has_z = k0 / 8 + cz < octets;
   const uint32_t y_off = (uint32_t)(ry * ld + min(n0 + 8 * cy, a.n_out - 1)) * (uint32_t)sizeof(T);
   const uint32_t z_off = (uint32_t)(rz * octets + my_octet) * 8u;
   const uint32_t e_off = (uint32_t)(rz * groups + (my_octet >> 2));
@@ -141,20 +140,33 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
       e[p - NY] = (a.exps + m * groups)[e_off];
     }
   };
-  auto load_any_rows = [&](int64_t step, int p) {
+  // The other steps' loads take the last row in place of the rows behind it, and the matrix's last 8
+  // columns where an octet ends behind them; store() puts that right.
+  auto load_edge = [&](int64_t step, int p) {
     if (p < NY) {
-      const int64_t m = step * C::kBM + C::kRowsN * p + ry;
-      y[p] = load_raw<DT>(static_cast<const T*>(a.dy.p) + m * ld, n0 + 8 * cy,
-                          m < a.rows ? a.n_out : 0);
+      const int64_t m = min(step * C::kBM + C::kRowsN * p + ry, a.rows - 1);
+      const T* row = static_cast<const T*>(a.dy.p) + m * ld;
+      if (a.n_out >= 8)
+        y[p] = load_raw<DT>(row + min(n0 + 8 * cy, a.n_out - 8));
+      else
+        y[p] = load_raw<DT>(row, n0 + 8 * cy, a.n_out);
     } else {
-      const int64_t m = step * C::kBM + C::kRowsK * (p - NY) + rz;
+      const int64_t m = min(step * C::kBM + C::kRowsK * (p - NY) + rz, a.rows - 1);
+      z[p - NY] = reinterpret_cast<const u2*>(a.codes)[m * octets + my_octet];
+      e[p - NY] = a.exps[m * groups + (my_octet >> 2)];
+    }
+  };
+  auto mend = [&](int64_t step, int p) {
+    if (p < NY) {
+      const int over = a.n_out >= 8 ? max(n0 + 8 * cy - (a.n_out - 8), 0) : 0;
+      uint32_t d[4 * Raw<DT>::kWords];
+      __builtin_memcpy(d, &y[p], sizeof d);
+      shift_down<4 * Raw<DT>::kWords>(d, (uint32_t)min(over, 7) * (sizeof(T) / 2));
+      __builtin_memcpy(&y[p], d, sizeof d);
+      if (step * C::kBM + C::kRowsN * p + ry >= a.rows) y[p] = Raw<DT>{};
+    } else if (step * C::kBM + C::kRowsK * (p - NY) + rz >= a.rows) {
       z[p - NY] = u2{0, 0};
       e[p - NY] = 0;
-      if (m < a.rows && has_z) {
-        const int64_t i = m * octets + k0 / 8 + cz;
-        z[p - NY] = reinterpret_cast<const u2*>(a.codes)[i];
-        e[p - NY] = a.exps[i >> 2];
-      }
     }
   };
   auto store = [&](short* stage, int p) {
@@ -184,6 +196,10 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
       f[i] = fragment(stage + fy_at + q * kPlane + 16 * p * C::kPitchN + 32 * i, C::kPitchN);
   };
 
+  // The straight loop below stores the steps first + 1 to lim - 2 and loads up to lim - 1, all whole.
+  const int64_t lim = whole < last ? whole : last;
+  auto loaded_whole = [&](int64_t step) { return first + 2 < lim && step > first && step < lim; };
+
   f16v acc[C::kFN][C::kFK] = {};
   b8 fz[C::kFK], fy[C::kFN];
   short *cur = s_mem, *nxt = s_mem + kStage;
@@ -210,17 +226,27 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
 #pragma unroll
       for (int t = 0; t < NY + NZ; ++t)
         if (t * (kPieces - 1) / (NY + NZ) == i) {
+          if (!all && more1 && !loaded_whole(s + 1)) mend(s + 1, t);
           if (more1) store(nxt, t);
           if (all)
             load_whole(s + 2, t);
           else if (more2)
-            load_any_rows(s + 2, t);
+            load_edge(s + 2, t);
         }
 #pragma unroll
       for (int u = 0; u < C::kFN; ++u)
 #pragma unroll
         for (int j = 0; j < C::kFK; ++j)
           acc[u][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy[u], fz[j], acc[u][j], 0, 0, 0);
+      // each matrix instruction followed by a share of the rest, which runs beside it
+#pragma unroll
+      for (int g = 0; g < C::kFN * C::kFK; ++g) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // vector
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // loads
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);   // LDS writes
+      }
 #pragma unroll
       for (int u = 0; u < C::kFN; ++u) fy[u] = ny[u];
       if (q + 1 == NS)
@@ -233,16 +259,22 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
   };
   if (first < last) {
 #pragma unroll
-    for (int p = 0; p < NY + NZ; ++p) load_any_rows(first, p);
+    for (int p = 0; p < NY + NZ; ++p) load_edge(first, p);
 #pragma unroll
-    for (int p = 0; p < NY + NZ; ++p) store(cur, p);
-    if (first + 1 < last)
+    for (int p = 0; p < NY + NZ; ++p) {
+      mend(first, p);
+      store(cur, p);
+    }
+    if (loaded_whole(first + 1)) {
 #pragma unroll
-      for (int p = 0; p < NY + NZ; ++p) load_any_rows(first + 1, p);
+      for (int p = 0; p < NY + NZ; ++p) load_whole(first + 1, p);
+    } else if (first + 1 < last) {
+#pragma unroll
+      for (int p = 0; p < NY + NZ; ++p) load_edge(first + 1, p);
+    }
     __syncthreads();
     read_z(cur, 0, fz);
     read_y(cur, 0, 0, fy);
-    const int64_t lim = whole < last ? whole : last;
     int64_t s = first;
     // nothing in flight: the loop's own waits then count its own loads only, in their order
     __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -250,34 +282,78 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
     for (; s < last; ++s) step(s, std::false_type());
   }
 
+  // Register r of a 32x32 product holds its row 8 * (r / 4) + 4 * (lane / 32) + r % 4, column
+  // lane % 32.  Only an accumulating call loads: its values one product ahead of the stores, which a
+  // wait for a load would otherwise wait for too.
   float* out = splits > 1 ? a.ws + (int64_t)blockIdx.y * a.n_out * a.cols : a.dw;
+  const bool add = splits == 1 && a.accumulate, scaled = splits == 1 && a.col_scale;
+  const bool inside = wide && k0 + C::kTK <= a.cols;
+  const int n_wave = n0 + wn + 4 * (lane >> 5), k_wave = k0 + wk + (lane & 31);
+  float* lane_out = out + (int64_t)n_wave * a.cols + k_wave;
+  constexpr int kProducts = C::kFN * C::kFK;
+  auto row = [](int t, int r) { return 32 * (t / C::kFK) + 8 * (r >> 2) + (r & 3); };
+  auto at = [&](int t, int r) { return lane_out + (int64_t)row(t, r) * a.cols + 32 * (t % C::kFK); };
+  auto within = [&](int t, int r) {
+    return n_wave + row(t, r) < a.n_out && k_wave + 32 * (t % C::kFK) < a.cols;
+  };
+  if (scaled)
 #pragma unroll
-  for (int j = 0; j < C::kFK; ++j) {
-    const int k = k0 + wk + 32 * j + (lane & 31);
-    if (k >= a.cols) continue;
-    const float sc = splits == 1 && a.col_scale ? load_any(a.col_scale, a.scale_dtype, k) : 1.0f;
+    for (int j = 0; j < C::kFK; ++j) {
+      const float sc = load_any(a.col_scale, a.scale_dtype, min(k_wave + 32 * j, a.cols - 1));
 #pragma unroll
-    for (int i = 0; i < C::kFN; ++i)
+      for (int i = 0; i < C::kFN; ++i) acc[i][j] *= sc;
+    }
+  if (add) {
+    float old[2][16] = {};
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int n = n0 + wn + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        if (n >= a.n_out) continue;
-        float* p = out + (int64_t)n * a.cols + k;
-        const float v = acc[i][j][r] * sc;
-        *p = splits == 1 && a.accumulate ? *p + v : v;
-      }
+    for (int t = 0; t <= kProducts; ++t) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (t < kProducts && within(t, r)) old[t & 1][r] = *at(t, r);
+      if (t == 0) continue;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (within(t - 1, r))
+          *at(t - 1, r) = old[(t - 1) & 1][r] + acc[(t - 1) / C::kFK][(t - 1) % C::kFK][r];
+    }
+  } else if (inside) {
+#pragma unroll
+    for (int t = 0; t < kProducts; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) *at(t, r) = acc[t / C::kFK][t % C::kFK][r];
+  } else {
+#pragma unroll
+    for (int t = 0; t < kProducts; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (within(t, r)) *at(t, r) = acc[t / C::kFK][t % C::kFK][r];
   }
 }
 
-// The parts of the row sum joined in order, scaled and stored.
+// The parts of the row sum joined in order, scaled and stored: kV neighbouring elements of a row a
+// thread.
+template <int kV>
 __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a, int splits) {
-  const int64_t total = (int64_t)a.n_out * a.cols;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t total = (uint32_t)a.n_out * (uint32_t)a.cols;   // below 2^31
+  const uint32_t i = (blockIdx.x * 256u + threadIdx.x) * kV;
   if (i >= total) return;
-  float v = a.ws[i];
-  for (int s = 1; s < splits; ++s) v += a.ws[s * total + i];
-  if (a.col_scale) v *= load_any(a.col_scale, a.scale_dtype, i % a.cols);
-  a.dw[i] = a.accumulate ? a.dw[i] + v : v;
+  float v[kV], w[kV];
+  __builtin_memcpy(v, a.ws + i, sizeof v);
+  for (int s = 1; s < splits; ++s) {
+    __builtin_memcpy(w, a.ws + (int64_t)s * total + i, sizeof w);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] += w[j];
+  }
+  if (a.col_scale)
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+      v[j] *= load_any(a.col_scale, a.scale_dtype, i % (uint32_t)a.cols + j);
+  if (a.accumulate) {
+    __builtin_memcpy(w, a.dw + i, sizeof w);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] += w[j];
+  }
+  __builtin_memcpy(a.dw + i, v, sizeof v);
 }
 
 // 128 KB and a bit of LDS: one workgroup of 8 waves a CU.  Values of several parts take half the rows a step.
@@ -331,8 +407,13 @@ hipError_t launch_wgrad(const WgradArgs& a, hipStream_t st) {
                      : a.dtype == kBF16 ? wgrad<kBF16>(a, s, st)
                                         : wgrad<kF16>(a, s, st))
     return e;
-  if (s.splits > 1)
-    k_wgrad_join<<<blocks_for((int64_t)a.n_out * a.cols, 256), 256, 0, st>>>(a, s.splits);
+  if (s.splits > 1) {
+    const int64_t total = (int64_t)a.n_out * a.cols;
+    if (a.cols % 4 == 0)
+      k_wgrad_join<4><<<blocks_for(total, 1024), 256, 0, st>>>(a, s.splits);
+    else
+      k_wgrad_join<1><<<blocks_for(total, 256), 256, 0, st>>>(a, s.splits);
+  }
   return hipGetLastError();
 }
 
