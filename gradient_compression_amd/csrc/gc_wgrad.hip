@@ -337,12 +337,16 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a, int splits) {
   const uint32_t total = (uint32_t)a.n_out * (uint32_t)a.cols;   // below 2^31
   const uint32_t i = (blockIdx.x * 256u + threadIdx.x) * kV;
   if (i >= total) return;
-  float v[kV], w[kV];
-  __builtin_memcpy(v, a.ws + i, sizeof v);
-  for (int s = 1; s < splits; ++s) {
-    __builtin_memcpy(w, a.ws + (int64_t)s * total + i, sizeof w);
+  float v[kV] = {}, w[kV];
+  for (int s = 0; s < splits; s += 8) {   // 8 parts in flight
+    float u[8][kV] = {};
 #pragma unroll
-    for (int j = 0; j < kV; ++j) v[j] += w[j];
+    for (int t = 0; t < 8; ++t)
+      if (s + t < splits) __builtin_memcpy(u[t], a.ws + (int64_t)(s + t) * total + i, sizeof w);
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[j] += u[t][j];
   }
   if (a.col_scale)
 #pragma unroll
@@ -356,14 +360,19 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a, int splits) {
   __builtin_memcpy(a.dw + i, v, sizeof v);
 }
 
-// 128 KB and a bit of LDS: one workgroup of 8 waves a CU.  Values of several parts take half the rows a step.
+// Values of several parts take half the rows a step, so that two stages fit the 160 KB of LDS.
 template <int DT>
 using Large = Tile<256, 256, 2, 4, DT == kBF16 ? 64 : 32>;
 template <int DT>
 using Small = Tile<128, 128, 2, 2, DT == kBF16 ? 64 : 32>;
+template <int DT>
+using Tiny = Tile<64, 64, 2, 2, DT == kBF16 ? 64 : 32>;
+
+enum TileKind { kLarge, kSmall, kTiny };
+constexpr int kTileSize[3] = {256, 128, 64};
 
 struct Shape {
-  bool large;
+  TileKind tile;
   int splits;
 };
 
@@ -371,15 +380,48 @@ int64_t tiles_of(int32_t n_out, int32_t cols, int t) {
   return (((int64_t)n_out + t - 1) / t) * (((int64_t)cols + t - 1) / t);
 }
 
-// Large tiles where they fill the 256 CUs; else small ones, the sum over the rows split so that
-// there are about 512 workgroups (two a CU), each of at least 2 steps.
+// A large tile needs the fewest loads and restores the fewest codes a product, but leaves CUs idle
+// where the matrix is small; a sum over many rows can be split over CUs, at the price of writing and
+// joining its parts.  The tile and the split with the least estimated time are taken.  A step of a
+// tile takes, with 1, 2 and 3 workgroups on its CU, in tenths of a microsecond (measured; a CU holds
+// 1 large, 2 small or 3 tiny ones):
+//              large   small      tiny
+//   bf16        17     9 14     5  8 11    (64 rows a step)
+//   fp16        14     9 11     5  6  8    (32 rows, 2 parts)
+//   fp32        25    12 17     8 10 13    (32 rows, 3 parts)
+// A call costs 4 us besides, a join 4 us, 0.1 us a part and its bytes (written and read) at 6 TB/s, or
+// at 4 where the parts pass 100 MB.  Against every
+// other choice, measured: 512 rows of 1024 x 1024 bf16 take tiny tiles, 7.9 us (small 11.5, small in
+// 4 parts 19.3); 8192 rows of 2048 x 2048 large ones in 4 parts, 84 us (small 115, tiny 152); 4096 rows
+// of 512 x 512 tiny ones in 8 parts, 15.5 us (whole 33.6).
 Shape shape_of(int64_t rows, int32_t n_out, int32_t cols, int dtype) {
-  if (tiles_of(n_out, cols, 256) >= 192) return {true, 1};
-  const int64_t tiles = tiles_of(n_out, cols, 128);
+  constexpr int kPerCU[3] = {1, 2, 3};
+  constexpr double kStepTime[3][3][3] = {   // by type (kF32, kBF16, kF16), tile, workgroups on the CU
+      {{2.5}, {1.2, 1.7}, {0.8, 1.0, 1.3}},
+      {{1.7}, {0.9, 1.4}, {0.5, 0.8, 1.1}},
+      {{1.4}, {0.9, 1.1}, {0.5, 0.6, 0.8}}};
+  constexpr int64_t kCUs = 256;
   const int64_t bm = dtype == kBF16 ? 64 : 32, steps = (rows + bm - 1) / bm;
-  int64_t s = tiles ? 512 / tiles : 1;
-  if (s > steps / 2) s = steps / 2;
-  return {false, s < 1 ? 1 : s > 16 ? 16 : (int)s};
+  Shape best = {kTiny, 1};
+  double least = 1e300;
+  for (int t = 0; t < 3; ++t) {
+    const int64_t tiles = tiles_of(n_out, cols, kTileSize[t]);
+    for (int s = 1; s <= 64 && (s == 1 || s <= steps); s += s < 4 ? 1 : s / 2) {
+      const int64_t groups = tiles * s, full = groups / (kCUs * kPerCU[t]);
+      const int64_t rest = groups - full * kCUs * kPerCU[t];
+      const double* step = kStepTime[dtype][t];
+      double us = full * step[kPerCU[t] - 1];
+      if (rest) us += step[(rest + kCUs - 1) / kCUs - 1];
+      us = us * (double)((steps + s - 1) / s) + 4.0;
+      const double bytes = 4.0 * s * (double)n_out * (double)cols;
+      if (s > 1) us += 4.0 + 0.1 * s + 2.0 * bytes / (bytes > 100e6 ? 4e6 : 6e6);
+      if (us < least) {
+        least = us;
+        best = {(TileKind)t, s};
+      }
+    }
+  }
+  return best;
 }
 
 template <int DT, typename C>
@@ -391,7 +433,9 @@ hipError_t wgrad(const WgradArgs& a, int splits, hipStream_t st) {
 
 template <int DT>
 hipError_t wgrad(const WgradArgs& a, const Shape& s, hipStream_t st) {
-  return s.large ? wgrad<DT, Large<DT>>(a, s.splits, st) : wgrad<DT, Small<DT>>(a, s.splits, st);
+  return s.tile == kLarge   ? wgrad<DT, Large<DT>>(a, s.splits, st)
+         : s.tile == kSmall ? wgrad<DT, Small<DT>>(a, s.splits, st)
+                            : wgrad<DT, Tiny<DT>>(a, s.splits, st);
 }
 
 }  // namespace

@@ -421,7 +421,8 @@ def test_weight_grad_of_many_tiles(dtype):
     """Matrices that fill the GPU with the largest tiles, whole and ragged ones, sums of no, one, two
     and several steps."""
     for n, (rows, n_out, cols) in enumerate([(1, 3600, 3400), (70, 3585, 3600), (129, 3840, 3328),
-                                             (200, 8200, 1800), (64, 300, 30000)]):
+                                             (200, 8200, 1800), (64, 300, 30000), (4000, 600, 520),
+                                             (3000, 1030, 1500)]):
         log(f"[wgrad] {dtype} {rows} {n_out}x{cols}")
         dy, codes, exps, want = exact_case(rows, n_out, cols, dtype, n)
         dw = torch.ones(n_out, cols, device="cuda")
