@@ -566,6 +566,9 @@ def _like(t, name, dev, like, like_name):
     """(pointer, row pitch) of a matrix of the shape and type of another; NULL for None."""
     if t is None:
         return None, 0
+    if (isinstance(t, _types[1]) and t.get_device() == dev and t.dtype == like.dtype
+            and t.shape == like.shape and t.is_contiguous()):
+        return t.data_ptr(), t.size(-1)
     p, ld, _, _, _ = _matrix(t, name, dev)
     if t.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
