@@ -231,16 +231,17 @@ __device__ __forceinline__ u2 encode8(const float (&v)[8], uint64_t block, uint3
   return e == kExpBad ? u2{0, 0} : r;
 }
 
-// code * scale for 8 codes, exact (7 bits and a sign times a power of two).  u = code + 128 is a byte,
-// which one instruction makes a float, and u * scale - 128 * scale rounds nothing; for a bad group
-// it is Inf - Inf, the NaN that it stands for.
+// code * scale for 8 codes, exact (7 bits and a sign times a power of two).  u = 127 - code is a byte
+// (the code's low 7 bits flipped), which one instruction makes a float, and 127 * scale - u * scale
+// rounds nothing: 127 times the largest scale is finite.  For a bad group it is Inf - Inf, the NaN
+// that it stands for.
 __device__ __forceinline__ void decode8(u2 c, float scale, float (&v)[8]) {
-  const float shift = -128.0f * scale;
+  const float top = 127.0f * scale;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t u = c[h] ^ 0x80808080u;
+    const uint32_t u = c[h] ^ 0x7F7F7F7Fu;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[4 * h + j] = fmaf((float)((u >> (8 * j)) & 0xFFu), scale, shift);
+    for (int j = 0; j < 4; ++j) v[4 * h + j] = fmaf((float)((u >> (8 * j)) & 0xFFu), -scale, top);
   }
 }
 

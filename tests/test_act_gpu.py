@@ -131,6 +131,29 @@ def test_quant_ends_of_the_range():
     assert nan.sum() == 128
 
 
+def test_every_exponent_is_read_back_exactly():
+    """All scales that are written, with all codes, through each reader: the restored matrix, the
+    norm's weight gradient and the weight gradient of one row of ones."""
+    codes = torch.arange(-127, 129, dtype=torch.int16).clamp(max=127).to(torch.int8).cuda()
+    for e in list(range(7, 12)) + [60, 120, 127, 128, 200] + list(range(244, 249)):
+        c = codes.view(1, 256)
+        x = torch.full((1, 8), e, dtype=torch.uint8, device="cuda")
+        want = torch.from_numpy(oracle.act_restore(c.cpu().numpy(), x.cpu().numpy(), 256))
+        assert torch.isfinite(want).all()
+        for t in (torch.float32, torch.bfloat16):
+            out = torch.empty(1, 256, dtype=t, device="cuda")
+            gca.act_restore(c, x, out)
+            assert torch.equal(out.float().cpu(), want), f"exponent {e} as {t}"
+        one = torch.ones(1, 256, device="cuda")
+        dx, dw = torch.empty_like(one), torch.empty(256, device="cuda")
+        gca.rmsnorm_backward(one, c, x, one[0, :1], dx, dweight=dw)
+        assert torch.equal(dw.cpu(), want[0]), f"exponent {e} in the norm"
+        for t in TYPES.values():
+            dl = torch.empty(3, 256, device="cuda")
+            gca.act_weight_grad(one[:, :3].to(t), c, x, dl)
+            assert torch.equal(dl.cpu(), want.expand(3, 256)), f"exponent {e} in the product of {t}"
+
+
 def test_quant_of_leading_dimensions_and_empty():
     x = activations(6, 70, "bf16", 4)
     codes, exps = check_quant(x, False, "flat")
