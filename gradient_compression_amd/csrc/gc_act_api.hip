@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMostRows = (int64_t)1 << 25;      // threads of a launch stay below 2^32
 constexpr int64_t kMostCodes = (int64_t)1 << 34;
+constexpr int64_t kMostCols = (int64_t)1 << 27;
 constexpr int64_t kMostWeights = ((int64_t)1 << 31) - 1;
 
 int64_t groups_of(int64_t cols) { return cols / 32 + (cols % 32 != 0); }
@@ -37,9 +38,12 @@ bool share_bytes(const Area& a, const Area& b) {
   const uintptr_t a1 = a0 + (a.rows - 1) * a.pitch + a.width;
   const uintptr_t b1 = b0 + (b.rows - 1) * b.pitch + b.width;
   if (a0 >= b1 || b0 >= a1) return false;
-  if (a.rows == 1 || b.rows == 1 || a.pitch != b.pitch) return true;
-  // column blocks of one wider matrix: disjoint when b's block lies in the gap of a's rows
-  const int64_t d = (int64_t)((b0 - a0) % (uintptr_t)a.pitch + a.pitch) % a.pitch;
+  // Their spans meet.  Pieces at one pitch (column blocks of a wider matrix), or one piece against
+  // rows, still share nothing where they lie in the rows' gaps.
+  if (a.rows == 1 && b.rows > 1) return share_bytes(b, a);
+  if (a.rows == 1 || (b.rows > 1 && a.pitch != b.pitch)) return true;
+  int64_t d = ((int64_t)b0 - (int64_t)a0) % a.pitch;   // b's place in a's row, 0 <= d < pitch
+  if (d < 0) d += a.pitch;
   return d < a.width || d + b.width > a.pitch;
 }
 
@@ -67,7 +71,7 @@ bool clash(std::initializer_list<Area> areas, std::initializer_list<std::pair<in
 
 int check_sizes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0) return GC_ERR_INVALID_ARG;
-  if (rows > kMostRows || cols > kMostWeights) return GC_ERR_UNSUPPORTED;
+  if (rows > kMostRows || cols > kMostCols) return GC_ERR_UNSUPPORTED;
   if (rows * groups_of(cols) * 32 > kMostCodes) return GC_ERR_UNSUPPORTED;   // < 2^57: no wrap
   return GC_OK;
 }
@@ -97,7 +101,7 @@ extern "C" {
 
 int gc_act_layout(int64_t cols, int64_t* pitch, int64_t* groups) {
   if (cols < 0) return GC_ERR_INVALID_ARG;
-  if (cols > kMostWeights) return GC_ERR_UNSUPPORTED;
+  if (cols > kMostCols) return GC_ERR_UNSUPPORTED;
   if (pitch) *pitch = groups_of(cols) * 32;
   if (groups) *groups = groups_of(cols);
   return GC_OK;
@@ -237,7 +241,7 @@ int gc_act_weight_grad_workspace(int64_t rows, int64_t n_out, int64_t cols, int3
                                  int64_t* bytes) {
   if (!bytes || !valid_dtype(dtype) || n_out < 0) return GC_ERR_INVALID_ARG;
   if (int rc = check_sizes(rows, cols)) return rc;
-  if (n_out > kMostWeights || n_out * cols > kMostWeights) return GC_ERR_UNSUPPORTED;
+  if (n_out > kMostCols || n_out * cols > kMostWeights) return GC_ERR_UNSUPPORTED;
   const int splits = gc::wgrad_splits(rows, (int32_t)n_out, (int32_t)cols, dtype);
   *bytes = splits > 1 ? (int64_t)splits * n_out * cols * 4 : 0;
   return GC_OK;

@@ -394,18 +394,19 @@ int gc_decompress_gathered(const gc_plan* plan, int32_t n_workers, const float* 
  *         bits) at counter (i / 4 low, i / 4 high, step low 32, 0x54), i = row * pitch + column:
  *         the restored value's expectation is x;
  *   a group that holds Inf or NaN, or A > 127 * 2^121: b = 255 and codes 0.
- * Restored value: code * 2^(b - 127), exact in fp32 and in bf16 (a group of b = 255 is NaN).  The
+ * Restored value: code * 2^(b - 127), exact in fp32 and in bf16 (a group of b = 255 is NaN; other
+ * bytes above 248 are not written and what they restore to is unspecified).  The
  * error is at most 2^(e-1) (nearest), below 2^e (stochastic); 2^e < A / 63.
  *
  * Matrices are row-major with unit column stride and a row pitch `ld` in elements (ld >= cols),
  * of a gc_dtype.  No alignment beyond the element's is required of them; 16-byte aligned rows
  * (pointer and pitch) are faster.  Rows or columns of 0 are allowed.  Sums are in fp32 (the norm's
  * square sum in double) in an order that depends on the sizes alone, so that repeated calls give
- * the same bits.  These calls keep nothing between calls; a workspace belongs to one call at a
- * time.  An output may be the very same matrix (pointer and pitch) as an input where stated; any
+ * the same bits.  The calls run on the current device, which the buffers must belong to, and keep
+ * nothing between calls; a workspace belongs to one call at a time.  An output may be the very same matrix (pointer and pitch) as an input where stated; any
  * other shared byte between an output and another buffer is an error.
- * Limits (GC_ERR_UNSUPPORTED beyond them): rows <= 2^25, rows * pitch <= 2^34, cols and n_out
- * < 2^31, n_out * cols < 2^31, cols <= 32768 for the norm.
+ * Limits (GC_ERR_UNSUPPORTED beyond them): rows <= 2^25, cols and n_out <= 2^27, rows * pitch
+ * <= 2^34, n_out * cols < 2^31, cols <= 32768 for the norm.
  * Errors: GC_ERR_INVALID_ARG (nothing launched), GC_ERR_UNSUPPORTED, GC_ERR_HIP.
  */
 typedef enum { GC_F32 = 0, GC_BF16 = 1, GC_F16 = 2 } gc_dtype;

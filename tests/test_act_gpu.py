@@ -250,6 +250,23 @@ def test_norm_strided_and_in_place(dtype):
         assert torch.equal(x4, y4)
 
 
+@pytest.mark.parametrize("gap", [0, 1, 6])
+def test_norm_between_column_blocks_of_one_buffer(gap):
+    """x, the residual, h and y side by side in the rows of one buffer: they share no byte."""
+    rows, cols = 7, 75
+    wide = torch.full((rows, 4 * (cols + gap)), 7.0, device="cuda")
+    x, res, h, y = (wide[:, i * (cols + gap):i * (cols + gap) + cols] for i in (2, 0, 3, 1))
+    x.copy_(activations(rows, cols, "f32", 1))
+    res.copy_(activations(rows, cols, "f32", 2))
+    want_h, want_y = torch.empty(rows, cols, device="cuda"), torch.empty(rows, cols, device="cuda")
+    gca.rmsnorm(x.contiguous(), residual=res.contiguous(), h=want_h, y=want_y)
+    gca.rmsnorm(x, residual=res, h=h, y=y)
+    assert torch.equal(h, want_h) and torch.equal(y, want_y)
+    assert bool((wide.view(rows, 4, -1)[:, :, cols:] == 7.0).all())
+    with pytest.raises(gca.GCError):
+        gca.rmsnorm(x, residual=res, y=wide[:, 1:1 + cols])
+
+
 def test_norm_of_rows_without_a_norm():
     # zeros, huge, tiny, Inf and NaN rows next to an ordinary one
     x = torch.randn(8, 100, generator=torch.Generator().manual_seed(1))

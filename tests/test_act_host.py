@@ -38,6 +38,10 @@ def quant(x=A, ld=64, dtype=1, rows=4, cols=64, rounding=0, codes=B, exps=C):
     (dict(rows=(1 << 25) + 1, cols=32), UNSUPPORTED),
     (dict(rows=1 << 25, cols=513, ld=513), UNSUPPORTED),
     (dict(cols=1 << 31, ld=1 << 31), UNSUPPORTED),
+    (dict(cols=(1 << 27) + 1, ld=1 << 28), UNSUPPORTED),
+    # odd pitches, the second buffer in front of the first, behind it, and inside a row
+    (dict(ld=77, codes=A - 160), BAD), (dict(ld=77, exps=A + 77 * 2 - 8 + 1), BAD),
+    (dict(ld=77, exps=A - 5), BAD),
     (dict(rows=0, x=None, codes=None, exps=None), OK),
     (dict(cols=0, x=None, codes=None, exps=None), OK),
 ])
@@ -74,6 +78,9 @@ def norm(x=A, ld_x=64, res=B, ld_r=64, dtype=1, rows=4, cols=64, w=C, wd=0, eps=
     (dict(h=A, ld_h=72), BAD),                   # the same place with another pitch
     (dict(h=A + 2), BAD), (dict(y=C), BAD), (dict(rstd=A), BAD), (dict(codes=A), BAD),
     (dict(y=B + 128 * 3 + 126), BAD),            # shares the residual's last element
+    # column blocks of one matrix that meet by one element, from either side
+    (dict(ld_x=130, ld_y=130, y=A + 126), BAD), (dict(ld_x=130, ld_y=130, y=A - 126), BAD),
+    (dict(ld_x=130, ld_y=130, y=A + 130 * 2 - 126), BAD),
     (dict(cols=32769, ld_x=40000, ld_r=40000, ld_h=40000, ld_y=40000), UNSUPPORTED),
     (dict(rows=1 << 26), UNSUPPORTED), (dict(rows=-1), BAD),
     (dict(rows=0), OK), (dict(cols=0), OK),
