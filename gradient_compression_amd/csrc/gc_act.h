@@ -50,10 +50,16 @@ struct Raw {
   static constexpr int kWords = sizeof(typename Elt<DT>::T) / 2;   // of 16 bytes
   u4 w[kWords];
 };
-template <int DT>
+typedef u4 __attribute__((aligned(2))) u4_at_any;
+// kStream: marked non-temporal, for what is read once and is too large to be in a cache.
+template <int DT, bool kStream = false>
 __device__ __forceinline__ Raw<DT> load_raw(const void* p) {
   Raw<DT> r;
-  __builtin_memcpy(&r, p, sizeof r);
+#pragma unroll
+  for (int i = 0; i < Raw<DT>::kWords; ++i) {
+    const u4_at_any* q = static_cast<const u4_at_any*>(p) + i;
+    r.w[i] = kStream ? __builtin_nontemporal_load(q) : *q;
+  }
   return r;
 }
 // Moves the words down by n halves of a word (n < 2 N), zeros from the top.
@@ -75,10 +81,10 @@ __device__ __forceinline__ void shift_down(uint32_t (&d)[N], uint32_t n) {
 
 // 8 columns from col of the row at p, zeros from `cols` on.  Where the row ends inside the octet its
 // last 8 columns are loaded and moved into place: one load, as everywhere else.
-template <int DT>
+template <int DT, bool kStream = false>
 __device__ __forceinline__ Raw<DT> load_raw(const typename Elt<DT>::T* p, int col, int cols) {
   constexpr int kWords = 4 * Raw<DT>::kWords, kHalves = sizeof(typename Elt<DT>::T) / 2;
-  if (col + 8 <= cols) return load_raw<DT>(p + col);
+  if (col + 8 <= cols) return load_raw<DT, kStream>(p + col);
   Raw<DT> r = {};
   if (col >= cols) return r;
   uint32_t d[kWords] = {};
@@ -151,15 +157,24 @@ __device__ __forceinline__ typename Elt<DT>::T round_to(float x) {
   return (typename Elt<DT>::T)x;
 }
 
-// Rounds v to the type and stores the columns below `cols`.
-template <int DT>
+// Rounds v to the type and stores the columns below `cols`, non-temporal where kStream.
+template <int DT, bool kStream = false>
 __device__ __forceinline__ void store8(typename Elt<DT>::T* p, int col, int cols,
                                        const float (&v)[8]) {
   typename Elt<DT>::T raw[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) raw[j] = round_to<DT>(v[j]);
   if (col + 8 <= cols) {
-    __builtin_memcpy(p + col, raw, sizeof raw);
+    Raw<DT> r;
+    __builtin_memcpy(&r, raw, sizeof r);
+#pragma unroll
+    for (int i = 0; i < Raw<DT>::kWords; ++i) {
+      u4_at_any* q = reinterpret_cast<u4_at_any*>(p + col) + i;
+      if (kStream)
+        __builtin_nontemporal_store(r.w[i], q);
+      else
+        *q = r.w[i];
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)

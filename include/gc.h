@@ -401,10 +401,11 @@ int gc_decompress_gathered(const gc_plan* plan, int32_t n_workers, const float* 
  * Matrices are row-major with unit column stride and a row pitch `ld` in elements (ld >= cols),
  * of a gc_dtype.  No alignment beyond the element's is required of them; 16-byte aligned rows
  * (pointer and pitch) are faster.  Rows or columns of 0 are allowed.  Sums are in fp32 (the norm's
- * square sum in double) in an order that depends on the sizes alone, so that repeated calls give
- * the same bits.  The calls run on the current device, which the buffers must belong to, and keep
- * nothing between calls; a workspace belongs to one call at a time.  An output may be the very same matrix (pointer and pitch) as an input where stated; any
- * other shared byte between an output and another buffer is an error.
+ * square sum in double) in an order that depends on the sizes and types alone, so that repeated
+ * calls give the same bits.  The calls run on the current device, which the buffers must belong to,
+ * and keep nothing between calls; a workspace belongs to one call at a time.  An output may be the
+ * very same matrix (pointer and pitch) as an input where stated; any other shared byte between an
+ * output and another buffer is an error.
  * Limits (GC_ERR_UNSUPPORTED beyond them): rows <= 2^25, cols and n_out <= 2^27, rows * pitch
  * <= 2^34, n_out * cols < 2^31, cols <= 32768 for the norm.
  * Errors: GC_ERR_INVALID_ARG (nothing launched), GC_ERR_UNSUPPORTED, GC_ERR_HIP.
