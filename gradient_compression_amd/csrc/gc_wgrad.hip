@@ -5,6 +5,15 @@
 // the bf16 matrix cores with exact operands: dY in bf16 as it is, in fp16 as two bf16 parts, in
 // fp32 as three (8 bits each, cut off the top one after the other, so that their sum is the value).
 // Products of two bf16 are exact in fp32, the sums are in fp32.
+//
+// Both operands have the summed dimension as their slow one, so they are staged in LDS as they lie
+// in memory, the codes restored on the way (once for a tile's 256 columns of dY), and read across
+// their rows by LDS's transposing reads.  Measured: 8192 x 11008 x 4096 bf16 in 0.67 to 0.77 ms (960 to
+// 1100 TFLOP/s; a library product of bf16 operands in this layout reaches 950 on that shape), 4096
+// x 4096 x 4096 in 0.13 to 0.15 ms.  The matrix cores are busy for 56 % of the cycles; LDS (no bank
+// conflicts) for 35 %; the clock is held at 1.8 to 1.9 GHz by the card's power, so that the energy
+// of a step sets its time more than its schedule does: tiles with more loads a product (256 x 128)
+// took 11 % longer, without any restoring a step took 7 % less.
 #include <type_traits>
 
 #include "gc_act_internal.h"
@@ -84,14 +93,18 @@ __device__ __forceinline__ void store_parts(short* y, int plane, const Raw<DT>& 
 }
 
 // Tile of this workgroup.  Workgroups go to the 8 XCDs in turn: each XCD gets a contiguous range of
-// the order below, in which 8 tiles along n share their part of Z, and its L2 holds what they share.
+// the order below, in which kBand tiles along n share their part of Z, and its L2 holds what they
+// share.  The 32 large tiles that run on an XCD read least where they are 4 along n (2 or 4 bytes an
+// element) by 8 along k (1 byte): 1096 us for 8192 x 8192 x 8192 bf16, with 8 along n 1108, with 2
+// 1114.
+constexpr int kBand = 4;
 __device__ __forceinline__ void tile_of(int tiles_n, int tiles_k, int* tn, int* tk) {
   const int total = tiles_n * tiles_k, id = blockIdx.x;
   const int q = total / 8, r = total % 8, xcd = id % 8, i = id / 8;
   const int t = xcd < r ? xcd * (q + 1) + i : r * (q + 1) + (xcd - r) * q + i;
-  const int band = t / (8 * tiles_k), high = min(8, tiles_n - 8 * band);
-  const int in = t - band * 8 * tiles_k;
-  *tn = 8 * band + in % high;
+  const int band = t / (kBand * tiles_k), high = min(kBand, tiles_n - kBand * band);
+  const int in = t - band * kBand * tiles_k;
+  *tn = kBand * band + in % high;
   *tk = in / high;
 }
 
