@@ -84,9 +84,10 @@ __device__ __forceinline__ void store_parts(short* y, int plane, const Raw<DT>& 
       if (q + 1 < parts<DT>())
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          // what is left under the 8 bits just taken; nothing is left of Inf and NaN
-          const float top = __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);
-          v[j] = mag_key(v[j]) < 0x7F800000u ? v[j] - top : 0.0f;
+          // what is left under the 8 bits just taken; nothing is left of Inf (Inf - Inf) and NaN,
+          // and what is left of a finite value is finite
+          v[j] = v[j] - __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);
+          if (q == 0 && v[j] != v[j]) v[j] = 0.0f;
         }
     }
   }
