@@ -154,8 +154,8 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
       e[p - NY] = (a.exps + m * groups)[e_off];
     }
   };
-  // The other steps' loads take the last row in place of the rows behind it, and the matrix's last 8
-  // columns where an octet ends behind them; store() puts that right.
+  // The same of any step, without a branch: the last row in place of the rows behind it, and the row's
+  // last 8 columns where an octet ends behind them; mend() puts that right.
   auto load_edge = [&](int64_t step, int p) {
     if (p < NY) {
       const int64_t m = min(step * C::kBM + C::kRowsN * p + ry, a.rows - 1);
@@ -170,6 +170,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_wgrad(WgradArgs a, int split
       e[p - NY] = a.exps[m * groups + (my_octet >> 2)];
     }
   };
+  // Moves such an octet into place, and clears the rows behind the last one.
   auto mend = [&](int64_t step, int p) {
     if (p < NY) {
       const int over = a.n_out >= 8 ? max(n0 + 8 * cy - (a.n_out - 8), 0) : 0;
