@@ -468,7 +468,8 @@ int gc_rmsnorm_backward(const void* dy, int64_t ld_dy, int32_t dtype, int64_t ro
  * The weight gradient of a linear layer whose input was kept (z the restored values):
  *   dweight[n][k] (+)= col_scale[k] * sum over the rows m of dy[m][n] * z[m][k]
  * with exact products (dy of any type and z are multiplied without rounding either) and fp32
- * sums; a part of an fp32 dy below 2^-126 may count as 0.
+ * sums; values (or the low bits of a value) of dy, products and sums below 2^-126 in magnitude may
+ * count as 0.
  *   dy        : rows x n_out of dtype.  col_scale : [cols] of scale_dtype, or NULL (1).
  *   dweight   : float[n_out][cols], any 4-byte alignment (a segment of the flat gradient);
  *               added to with accumulate != 0, else overwritten (with 0 for rows = 0).

@@ -250,6 +250,41 @@ def test_norm_strided_and_in_place(dtype):
         assert torch.equal(x4, y4)
 
 
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_norm_outputs_are_optional_and_shapes_have_leading_dimensions(dtype):
+    shape, cols = (3, 5, 130), 130
+    x, res = (activations(15, cols, dtype, i).view(shape) for i in (1, 2))
+    w = torch.rand(cols, device="cuda").to(torch.float16)
+    h, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(3, 5, device="cuda")
+    codes, exps = checkpoint(14, cols)
+    gca.rmsnorm(x, weight=w, residual=res, h=h, y=y, rstd=rstd, codes=codes, exps=exps)
+    for only in (("y",), ("codes", "exps"), ("h", "y"), ("codes", "exps", "rstd"), ("h", "codes", "exps")):
+        got = dict(h=torch.empty_like(x), y=torch.empty_like(x), rstd=torch.empty_like(rstd),
+                   codes=torch.empty_like(codes), exps=torch.empty_like(exps))
+        gca.rmsnorm(x, weight=w, residual=res, **{k: got[k] for k in only})
+        for k in only:
+            assert torch.equal(got[k], dict(h=h, y=y, rstd=rstd, codes=codes, exps=exps)[k]), (only, k)
+    with pytest.raises(gca.GCError):
+        gca.rmsnorm(x, h=h)
+    with pytest.raises(ValueError):
+        gca.rmsnorm(x, codes=codes)
+    with pytest.raises(ValueError):
+        gca.rmsnorm(x, y=y.view(15, cols))
+    with pytest.raises(TypeError):
+        gca.rmsnorm(x, y=y, residual=res.double())
+    with pytest.raises(ValueError):
+        gca.rmsnorm(x, y=y, weight=w[:-1])
+    dx, dw, flat = torch.empty_like(x), torch.empty(cols, device="cuda"), torch.empty(15, cols, dtype=x.dtype, device="cuda")
+    dw2 = torch.empty_like(dw)
+    gca.rmsnorm_backward(y, codes, exps, rstd, dx, weight=w, dres=h, dweight=dw)
+    gca.rmsnorm_backward(y.view(15, cols), codes, exps, rstd, flat, weight=w, dres=h.view(15, cols), dweight=dw2)
+    assert torch.equal(dx.view(15, cols), flat) and torch.equal(dw, dw2)
+    dl, dl2 = torch.empty(70, cols, device="cuda"), torch.empty(70, cols, device="cuda")
+    gca.act_weight_grad(x[..., :70], codes, exps, dl)
+    gca.act_weight_grad(x.reshape(15, cols)[:, :70].contiguous(), codes, exps, dl2)
+    assert torch.equal(dl, dl2)
+
+
 @pytest.mark.parametrize("gap", [0, 1, 6])
 def test_norm_between_column_blocks_of_one_buffer(gap):
     """x, the residual, h and y side by side in the rows of one buffer: they share no byte."""

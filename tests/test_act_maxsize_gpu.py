@@ -91,3 +91,45 @@ def test_weight_grad_over_a_long_batch():
     for a in range(0, rows, 20_000):          # whole numbers below 2^24: exact in fp32
         want += (dy[a:a + 20_000].float().t().contiguous() @ codes[a:a + 20_000].float()).double()
     assert torch.equal(dw.double(), want)
+
+
+def whole(shape, most, dtype=torch.float32):
+    return torch.randint(-most, most + 1, shape, device="cuda").to(dtype)
+
+
+def test_weight_grad_of_far_apart_rows():
+    """Rows of dy further apart than 2^24 elements, and a checkpoint row of more than 2^25 columns."""
+    ld = (1 << 24) + 40
+    buf = torch.zeros(5 * ld, dtype=torch.bfloat16, device="cuda")
+    dy = buf.as_strided((5, 200), (ld, 1), 3)
+    dy.copy_(whole((5, 200), 50))
+    codes = torch.randint(-50, 51, (5, 96), device="cuda", dtype=torch.int8)
+    exps = torch.full((5, 3), 127, dtype=torch.uint8, device="cuda")
+    dw = torch.empty(200, 96, device="cuda")
+    gca.act_weight_grad(dy, codes, exps, dw)
+    assert torch.equal(dw, dy.float().t().contiguous() @ codes.float())
+    cols = (1 << 25) + 70
+    pitch, groups = gca.act_layout(cols)
+    codes = torch.randint(-50, 51, (3, pitch), device="cuda", dtype=torch.int8)
+    exps = torch.full((3, groups), 127, dtype=torch.uint8, device="cuda")
+    dy = whole((3, 2), 50, torch.bfloat16)
+    dw = torch.empty(2, cols, device="cuda")
+    gca.act_weight_grad(dy, codes, exps, dw)
+    want = sum(dy[m].float()[:, None] * codes[m, :cols].float() for m in range(3))
+    assert torch.equal(dw, want)
+
+
+def test_weight_grad_of_the_largest_matrix():
+    n_out, cols, rows = 65536, 32767, 70         # 2^31 - 65536 weights
+    dy = whole((rows, n_out), 20, torch.bfloat16)
+    pitch, groups = gca.act_layout(cols)
+    codes = torch.randint(-20, 21, (rows, pitch), device="cuda", dtype=torch.int8)
+    exps = torch.full((rows, groups), 127, dtype=torch.uint8, device="cuda")
+    dw = torch.empty(n_out, cols, device="cuda")
+    log("[act max] largest weight matrix")
+    gca.act_weight_grad(dy, codes, exps, dw)
+    torch.cuda.synchronize()
+    z = codes[:, :cols].float()
+    for a in range(0, n_out, 8192):
+        want = dy[:, a:a + 8192].float().t().contiguous() @ z
+        assert torch.equal(dw[a:a + 8192], want), f"rows from {a}"
