@@ -508,12 +508,6 @@ def _load_types():
     return _types
 
 
-def _current_device():
-    torch = (_types or _load_types())[0]
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or \
-        torch.cuda.is_available() else -2
-
-
 def act_layout(cols: int):
     """(pitch, groups) of a checkpoint's rows: codes are int8[rows, pitch], exps uint8[rows,
     groups] (host-only)."""
@@ -529,6 +523,17 @@ def _refuse_place(t, name, dev):
     if t.device.type != "cuda":
         raise ValueError(f"{name} must live on the GPU")
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _device_of(t, name):
+    """The current device's index, which must be the tensor's."""
+    torch, Tensor = (_types or _load_types())[:2]
+    if not isinstance(t, Tensor) or t.get_device() < 0:
+        _refuse_place(t, name, None)
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        _refuse_place(t, name, dev)
+    return dev
 
 
 def _matrix(t, name, dev):
@@ -566,7 +571,7 @@ def _like(t, name, dev, like, like_name):
     """(pointer, row pitch) of a matrix of the shape and type of another; NULL for None."""
     if t is None:
         return None, 0
-    if (isinstance(t, _types[1]) and t.get_device() == dev and t.dtype == like.dtype
+    if (isinstance(t, _types[1]) and t.get_device() == dev and t.dtype is like.dtype
             and t.shape == like.shape and t.is_contiguous()):
         return t.data_ptr(), t.size(-1)
     p, ld, _, _, _ = _matrix(t, name, dev)
@@ -595,10 +600,16 @@ def _array(t, name, dtype, numel, dev):
 
 def _checkpoint(codes, exps, rows, cols, dev):
     """Pointers of the two arrays of a rows x cols checkpoint."""
-    torch = _types[0]
-    groups = -(-cols // ACT_GROUP)
-    return (_array(codes, "codes", torch.int8, rows * groups * ACT_GROUP, dev),
-            _array(exps, "exps", torch.uint8, rows * groups, dev))
+    torch, Tensor = _types[:2]
+    n = rows * -(-cols // ACT_GROUP)
+    if (isinstance(codes, Tensor) and isinstance(exps, Tensor) and n
+            and codes.dtype is torch.int8 and exps.dtype is torch.uint8
+            and codes.get_device() == dev and exps.get_device() == dev
+            and codes.numel() == n * ACT_GROUP and exps.numel() == n
+            and codes.is_contiguous() and exps.is_contiguous()):
+        return codes.data_ptr(), exps.data_ptr()
+    return (_array(codes, "codes", torch.int8, n * ACT_GROUP, dev),
+            _array(exps, "exps", torch.uint8, n, dev))
 
 
 def _columns(t, name, cols, dev):
@@ -642,7 +653,7 @@ def act_quant(x, codes, exps, stochastic: bool = False, seed: int = 0, step: int
               stream=None):
     """x into its 8-bit checkpoint: one power-of-two scale for 32 columns of a row, codes rounded
     to nearest even or, with ``stochastic``, by the Philox stream of (seed, step)."""
-    dev = _current_device()
+    dev = _device_of(x, "x")
     p, ld, rows, cols, code = _matrix(x, "x", dev)
     cp, ep = _checkpoint(codes, exps, rows, cols, dev)
     _check(lib().gc_act_quant(p, ld, code, rows, cols, 1 if stochastic else 0, int(seed) & _MASK64,
@@ -651,7 +662,7 @@ def act_quant(x, codes, exps, stochastic: bool = False, seed: int = 0, step: int
 
 def act_restore(codes, exps, out, stream=None):
     """out = the checkpoint's values, rounded to out's type (exact in float32 and bfloat16)."""
-    dev = _current_device()
+    dev = _device_of(out, "out")
     p, ld, rows, cols, code = _matrix(out, "out", dev)
     cp, ep = _checkpoint(codes, exps, rows, cols, dev)
     _check(lib().gc_act_restore(cp, ep, rows, cols, p, ld, code, _raw_stream(stream, dev)),
@@ -665,7 +676,7 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, h=None, y=None, rs
     8-bit checkpoint into (codes, exps).  ``h``, ``y``, ``rstd`` (float32[rows]) and the
     checkpoint are written where given (at least y or the checkpoint); h or y may be x or
     residual itself."""
-    dev = _current_device()
+    dev = _device_of(x, "x")
     xp, ld_x, rows, cols, code = _matrix(x, "x", dev)
     rp, ld_r = _like(residual, "residual", dev, x, "x")
     hp, ld_h = _like(h, "h", dev, x, "x")
@@ -697,7 +708,7 @@ def rmsnorm_backward(dy, codes, exps, rstd, dx, weight=None, dres=None, dweight=
     t = dy * weight; dweight (float32, a segment of the flat gradient) = sum over rows of dy * z,
     added to what it holds with ``accumulate``.  dx may be dy or dres itself.  ``workspace``: a
     tensor of rmsnorm_backward_workspace bytes; allocated for the call when None."""
-    dev = _current_device()
+    dev = _device_of(dy, "dy")
     p, ld, rows, cols, code = _matrix(dy, "dy", dev)
     if dx is None:
         raise TypeError("dx must be a torch tensor")
@@ -732,7 +743,7 @@ def act_weight_grad(dy, codes, exps, dweight, col_scale=None, accumulate: bool =
     cols], a segment of the flat gradient viewed so) is added to with ``accumulate``.
     ``workspace``: a tensor of act_weight_grad_workspace bytes; allocated for the call when
     None."""
-    dev = _current_device()
+    dev = _device_of(dy, "dy")
     p, ld, rows, n_out, code = _matrix(dy, "dy", dev)
     if not isinstance(dweight, _types[1]):
         raise TypeError("dweight must be a torch tensor")

@@ -28,6 +28,7 @@ struct Area {
   bool out;
 };
 Area matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int32_t dtype, bool out) {
+  if (!p || !rows || !cols) return {nullptr, 0, 0, 0, out};   // whatever ld is
   return {p, rows, cols * size_of(dtype), ld * size_of(dtype), out};
 }
 Area flat(const void* p, int64_t bytes, bool out) { return {p, bytes > 0, bytes, bytes, out}; }

@@ -44,6 +44,9 @@ def quant(x=A, ld=64, dtype=1, rows=4, cols=64, rounding=0, codes=B, exps=C):
     (dict(ld=77, exps=A - 5), BAD),
     (dict(rows=0, x=None, codes=None, exps=None), OK),
     (dict(cols=0, x=None, codes=None, exps=None), OK),
+    (dict(rows=0, ld=(1 << 63) - 1), OK), (dict(cols=0, ld=-(1 << 63)), OK),
+    (dict(ld=(1 << 63) - 1), BAD), (dict(ld=-(1 << 63)), BAD),
+    (dict(rows=(1 << 63) - 1), UNSUPPORTED), (dict(cols=(1 << 63) - 1), UNSUPPORTED),
 ])
 def test_quant_refuses(case, want):
     assert quant(**case) == want
@@ -120,6 +123,7 @@ def wgrad(dy=A, ld=64, dtype=1, rows=4, n_out=64, cols=64, codes=B, exps=C, sc=D
     (dict(ld=63), BAD), (dict(rows=-1), BAD), (dict(n_out=-1), BAD), (dict(cols=-1), BAD),
     (dict(dw=A), BAD), (dict(dw=B), BAD), (dict(dw=D), BAD), (dict(ws=F + 4), BAD),
     (dict(n_out=1 << 20, ld=1 << 20, cols=1 << 11), UNSUPPORTED),
+    (dict(n_out=(1 << 63) - 1), UNSUPPORTED), (dict(ld=(1 << 63) - 1), BAD), (dict(n=-1), BAD),
     (dict(n_out=0, dy=None, dw=None), OK), (dict(cols=0, dw=None), OK),
     (dict(rows=0, acc=1, dy=None, codes=None, exps=None, ws=None, n=0), OK),
 ])
