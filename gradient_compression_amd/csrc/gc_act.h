@@ -203,6 +203,8 @@ __device__ __forceinline__ float exponent_scale(uint32_t e) { return __uint_as_f
 // quad calls it.  x * 2^-e is exact, so the code of a value is the same however it was formed:
 // rounded to nearest even by adding 1.5 * 2^23, whose unit is 1; or, with kRandom, floor or
 // ceiling of the magnitude by the 24-bit draws of blocks `block` and `block + 1` (4 columns each).
+// The draw is compared with what the floor leaves in the value's own unit, u * 2^(e - 24) < |x| -
+// floor * 2^e, where both sides are exact; |x| / 2^e itself would be 0 where it is below 2^-149.
 template <bool kRandom>
 __device__ __forceinline__ u2 encode8(const float (&v)[8], uint64_t block, uint32_t seed_lo,
                                       uint32_t seed_hi, uint32_t step_lo, uint32_t* exponent) {
@@ -224,10 +226,11 @@ __device__ __forceinline__ u2 encode8(const float (&v)[8], uint64_t block, uint3
       w[4 + j] = w1[j] >> 8;
     }
     const float inv = __uint_as_float((254u - min(e, kExpHighest)) << 23);
+    const float scale = exponent_scale(min(e, kExpHighest)), unit = scale * 0x1p-24f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(v[j]) * inv, f = floorf(a);
-      const int m = (int)f + ((float)w[j] < (a - f) * 16777216.0f ? 1 : 0);
+      const float f = floorf(fabsf(v[j]) * inv);
+      const int m = (int)f + ((float)w[j] * unit < fmaf(-f, scale, fabsf(v[j])) ? 1 : 0);
       q[j] = (uint32_t)(signbit(v[j]) ? -m : m);
     }
   } else {
