@@ -277,7 +277,7 @@ int gc_act_weight_grad(const void* dy, int64_t ld_dy, int32_t dtype, int64_t row
   a.dy = mat(dy, ld_dy);
   a.codes = codes;
   a.exps = exps;
-  a.col_scale = col_scale;
+  a.col_scale = rows ? col_scale : nullptr;   // a sum of no rows is 0, whatever its scale
   a.dw = dweight;
   a.accumulate = accumulate != 0;
   a.ws = static_cast<float*>(workspace);

@@ -27,3 +27,17 @@ def test_stochastic_codes_of_values_far_below_their_group(dtype):
             gca.act_quant(x.cuda(), codes, exps, stochastic=True, seed=4, step=0)
             assert_bitwise(exps, want_e, f"{small} beside {top} exponents")
             assert_bitwise(codes, want_c, f"{small} beside {top} codes")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_weight_gradient_of_no_rows_is_zero_whatever_the_scale(dtype):
+    scale = torch.tensor([1.0, -2.0, float("inf"), float("nan"), -float("inf")], device="cuda").repeat(7)
+    none = torch.empty(0, 4, dtype=dtype, device="cuda")
+    codes = torch.empty(0, 64, dtype=torch.int8, device="cuda")
+    exps = torch.empty(0, 2, dtype=torch.uint8, device="cuda")
+    dw = torch.full((4, 35), 5.0, device="cuda")
+    gca.act_weight_grad(none, codes, exps, dw, col_scale=scale)
+    assert bool((dw == 0.0).all())
+    dw.fill_(5.0)
+    gca.act_weight_grad(none, codes, exps, dw, col_scale=scale, accumulate=True)
+    assert bool((dw == 5.0).all())
