@@ -493,8 +493,13 @@ def read_f32(x, sink, stream=None):
 # ------------------------------------------------------------ activation checkpoints (8 bits)
 # These calls are small beside a training step's but many, so their checks take the shortest way:
 # torch's names and the type codes are looked up once, pointers go to ctypes as integers.
+# Autograd records none of them: to it their outputs are constants, whether or not an input requires
+# a gradient.  They raise the version counters of what they write, so that a graph that saved a
+# tensor they overwrote says so in its backward pass.
 ACT_GROUP = 32        # columns that share a scale
-_types = None         # (torch, Tensor, {dtype: code}, current stream's handle) at the first call
+# (torch, Tensor, {dtype: code}, current stream's handle, raiser of versions, current device) at the
+# first call
+_types = None
 
 
 def _load_types():
@@ -503,8 +508,12 @@ def _load_types():
     # the current stream as an integer, where this torch can tell it without a Stream object
     handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    # the same calls without their wrappers' own checks, where this torch has them
+    device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    raise_versions = getattr(torch._C, "_increment_version", None) or \
+        torch.autograd.graph.increment_version
     _types = (torch, torch.Tensor,
-              {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, handle)
+              {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}, handle, raise_versions, device)
     return _types
 
 
@@ -527,11 +536,12 @@ def _refuse_place(t, name, dev):
 
 def _device_of(t, name):
     """The current device's index, which must be the tensor's."""
-    torch, Tensor = (_types or _load_types())[:2]
-    if not isinstance(t, Tensor) or t.get_device() < 0:
+    types = _types or _load_types()
+    at = t.get_device() if isinstance(t, types[1]) else -1
+    if at < 0:
         _refuse_place(t, name, None)
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
+    dev = types[5]()       # torch has set the GPU up: a tensor lives there
+    if at != dev:
         _refuse_place(t, name, dev)
     return dev
 
@@ -572,7 +582,7 @@ def _like(t, name, dev, like, like_name):
     if t is None:
         return None, 0
     if (isinstance(t, _types[1]) and t.get_device() == dev and t.dtype is like.dtype
-            and t.shape == like.shape and t.is_contiguous()):
+            and t.is_same_size(like) and t.is_contiguous()):
         return t.data_ptr(), t.size(-1)
     p, ld, _, _, _ = _matrix(t, name, dev)
     if t.dtype != like.dtype:
@@ -658,6 +668,7 @@ def act_quant(x, codes, exps, stochastic: bool = False, seed: int = 0, step: int
     cp, ep = _checkpoint(codes, exps, rows, cols, dev)
     _check(lib().gc_act_quant(p, ld, code, rows, cols, 1 if stochastic else 0, int(seed) & _MASK64,
                               int(step) & _MASK64, cp, ep, _raw_stream(stream, dev)), "gc_act_quant")
+    _types[4]((codes, exps))
 
 
 def act_restore(codes, exps, out, stream=None):
@@ -667,6 +678,7 @@ def act_restore(codes, exps, out, stream=None):
     cp, ep = _checkpoint(codes, exps, rows, cols, dev)
     _check(lib().gc_act_restore(cp, ep, rows, cols, p, ld, code, _raw_stream(stream, dev)),
            "gc_act_restore")
+    _types[4]((out,))
 
 
 def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, h=None, y=None, rstd=None,
@@ -691,6 +703,7 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, h=None, y=None, rs
                             ld_y, _array(rstd, "rstd", _types[0].float32, rows, dev), cp, ep,
                             1 if stochastic else 0, int(seed) & _MASK64, int(step) & _MASK64,
                             _raw_stream(stream, dev)), "gc_rmsnorm")
+    _types[4]([t for t in (h, y, rstd, codes, exps) if t is not None])
 
 
 @functools.lru_cache(maxsize=4096)
@@ -724,6 +737,7 @@ def rmsnorm_backward(dy, codes, exps, rstd, dx, weight=None, dres=None, dweight=
                                      _array(rstd, "rstd", f32, rows, dev), wp, wcode, rp, ld_r, xp,
                                      ld_x, dwp, 1 if accumulate else 0, ws, ws_bytes,
                                      _raw_stream(stream, dev)), "gc_rmsnorm_backward")
+    _types[4]((dx,) if dweight is None else (dx, dweight))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -758,6 +772,7 @@ def act_weight_grad(dy, codes, exps, dweight, col_scale=None, accumulate: bool =
     _check(lib().gc_act_weight_grad(p, ld, code, rows, n_out, cols, cp, ep, sp, scode, dwp,
                                     1 if accumulate else 0, ws, ws_bytes, _raw_stream(stream, dev)),
            "gc_act_weight_grad")
+    _types[4]((dweight,))
 
 
 __all__ = ["Plan", "GCError", "lib", "status_string", "copy_f32", "add_f32", "read_f32", "layout",

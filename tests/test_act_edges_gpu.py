@@ -41,3 +41,75 @@ def test_weight_gradient_of_no_rows_is_zero_whatever_the_scale(dtype):
     dw.fill_(5.0)
     gca.act_weight_grad(none, codes, exps, dw, col_scale=scale, accumulate=True)
     assert bool((dw == 5.0).all())
+
+
+class Buffers:
+    """What a block's calls read and write, 40 x 96 and a layer of 24 outputs."""
+
+    def __init__(self):
+        gen = torch.Generator("cuda").manual_seed(3)
+        self.x, self.res, self.dout = (torch.randn(40, n, generator=gen, device="cuda")
+                                       for n in (96, 96, 24))
+        self.w = torch.rand(96, generator=gen, device="cuda")
+        self.h, self.y, self.dx = (torch.empty_like(self.x) for _ in range(3))
+        self.rstd, self.dw = torch.empty(40, device="cuda"), torch.empty(96, device="cuda")
+        self.codes = torch.empty(40, 96, dtype=torch.int8, device="cuda")
+        self.exps = torch.empty(40, 3, dtype=torch.uint8, device="cuda")
+        self.flat = torch.empty(2 + 24 * 96, device="cuda")
+        self.dl = self.flat[1:-1].view(24, 96)
+
+    def calls(self):
+        """Each call with the names of what it writes."""
+        return [
+            (lambda: gca.rmsnorm(self.x, weight=self.w, residual=self.res, h=self.h, y=self.y,
+                                 rstd=self.rstd, codes=self.codes, exps=self.exps),
+             {"h", "y", "rstd", "codes", "exps"}),
+            (lambda: gca.rmsnorm(self.x, residual=self.res, h=self.res, y=self.x), {"x", "res"}),
+            (lambda: gca.act_quant(self.x, self.codes, self.exps), {"codes", "exps"}),
+            (lambda: gca.act_restore(self.codes, self.exps, self.h), {"h"}),
+            (lambda: gca.rmsnorm_backward(self.y, self.codes, self.exps, self.rstd, self.dx,
+                                          weight=self.w, dres=self.h), {"dx"}),
+            (lambda: gca.rmsnorm_backward(self.y, self.codes, self.exps, self.rstd, self.y,
+                                          dweight=self.dw), {"y", "dw"}),
+            (lambda: gca.act_weight_grad(self.dout, self.codes, self.exps, self.dl,
+                                         col_scale=self.w), {"dl", "flat"}),
+        ]
+
+
+def test_written_tensors_raise_their_version_and_no_others():
+    b = Buffers()
+    for i, (call, written) in enumerate(b.calls()):
+        before = {k: t._version for k, t in vars(b).items()}
+        call()
+        raised = {k for k, t in vars(b).items() if t._version != before[k]}
+        assert raised == written, f"call {i}"
+    with torch.inference_mode():       # such tensors have no version
+        b = Buffers()
+        for call, _ in b.calls():
+            call()
+
+
+@pytest.mark.parametrize("which", ["h", "x", "res", "dx", "dw", "dl"])
+def test_autograd_notices_a_saved_tensor_that_a_call_overwrote(which):
+    b = Buffers()
+    w = torch.ones((), device="cuda", requires_grad=True)
+    saved = torch.zeros_like(getattr(b, which))
+    loss = (saved * w).sum()           # keeps `saved` for w's gradient
+    setattr(b, which, saved)
+    for call, written in b.calls():
+        if which in written:
+            call()
+            break
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_outputs_are_constants_to_autograd():
+    b = Buffers()
+    b.x.requires_grad_()
+    b.w.requires_grad_()
+    gca.rmsnorm(b.x, weight=b.w, residual=b.res, h=b.h, y=b.y, rstd=b.rstd, codes=b.codes,
+                exps=b.exps)
+    assert not (b.h.requires_grad or b.y.requires_grad or b.rstd.requires_grad)
+    (b.y * b.w).sum().backward()
+    assert torch.equal(b.w.grad, b.y.sum(0)) and b.x.grad is None
