@@ -653,7 +653,11 @@ def _workspace(workspace, need, stream, dev):
 
 
 def _raw_stream(stream, dev):
-    return _types[3](dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _types[3](dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
 _MASK64 = 2 ** 64 - 1
@@ -732,11 +736,12 @@ def rmsnorm_backward(dy, codes, exps, rstd, dx, weight=None, dres=None, dweight=
     f32 = _types[0].float32
     dwp = _array(dweight, "dweight", f32, cols, dev)
     need = rmsnorm_backward_workspace(rows, cols) if dweight is not None else 0
+    st = _raw_stream(stream, dev)
     ws, ws_bytes, _keep = _workspace(workspace, need, stream, dev)
     _check(lib().gc_rmsnorm_backward(p, ld, code, rows, cols, cp, ep,
                                      _array(rstd, "rstd", f32, rows, dev), wp, wcode, rp, ld_r, xp,
-                                     ld_x, dwp, 1 if accumulate else 0, ws, ws_bytes,
-                                     _raw_stream(stream, dev)), "gc_rmsnorm_backward")
+                                     ld_x, dwp, 1 if accumulate else 0, ws, ws_bytes, st),
+           "gc_rmsnorm_backward")
     _types[4]((dx,) if dweight is None else (dx, dweight))
 
 
@@ -767,10 +772,11 @@ def act_weight_grad(dy, codes, exps, dweight, col_scale=None, accumulate: bool =
     dwp = _array(dweight, "dweight", _types[0].float32, n_out * cols, dev)
     cp, ep = _checkpoint(codes, exps, rows, cols, dev)
     sp, scode = _columns(col_scale, "col_scale", cols, dev)
+    st = _raw_stream(stream, dev)
     ws, ws_bytes, _keep = _workspace(
         workspace, act_weight_grad_workspace(rows, n_out, cols, dy.dtype), stream, dev)
     _check(lib().gc_act_weight_grad(p, ld, code, rows, n_out, cols, cp, ep, sp, scode, dwp,
-                                    1 if accumulate else 0, ws, ws_bytes, _raw_stream(stream, dev)),
+                                    1 if accumulate else 0, ws, ws_bytes, st),
            "gc_act_weight_grad")
     _types[4]((dweight,))
 

@@ -1,4 +1,6 @@
 """Calls of the activation operators at the edges of what their contract allows."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -113,3 +115,21 @@ def test_outputs_are_constants_to_autograd():
     assert not (b.h.requires_grad or b.y.requires_grad or b.rstd.requires_grad)
     (b.y * b.w).sum().backward()
     assert torch.equal(b.w.grad, b.y.sum(0)) and b.x.grad is None
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The workspace would be allocated there, and the kernel would run there."""
+    b = Buffers()
+    other = SimpleNamespace(device_index=torch.cuda.current_device() + 1, cuda_stream=0)
+    before = {k: t.clone() for k, t in vars(b).items()}
+    for call in (lambda: gca.act_quant(b.x, b.codes, b.exps, stream=other),
+                 lambda: gca.act_restore(b.codes, b.exps, b.h, stream=other),
+                 lambda: gca.rmsnorm(b.x, y=b.y, stream=other),
+                 lambda: gca.rmsnorm_backward(b.y, b.codes, b.exps, b.rstd, b.dx, dweight=b.dw,
+                                              stream=other),
+                 lambda: gca.act_weight_grad(b.dout, b.codes, b.exps, b.dl, stream=other)):
+        with pytest.raises(ValueError, match="stream is on"):
+            call()
+    torch.cuda.synchronize()
+    for k, t in vars(b).items():
+        assert torch.equal(t.view(torch.uint8), before[k].view(torch.uint8)), k
