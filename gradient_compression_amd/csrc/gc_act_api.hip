@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <numeric>
 #include <utility>
 
 #include "gc.h"
@@ -39,13 +40,16 @@ bool share_bytes(const Area& a, const Area& b) {
   const uintptr_t a1 = a0 + (a.rows - 1) * a.pitch + a.width;
   const uintptr_t b1 = b0 + (b.rows - 1) * b.pitch + b.width;
   if (a0 >= b1 || b0 >= a1) return false;
-  // Their spans meet.  Pieces at one pitch (column blocks of a wider matrix), or one piece against
-  // rows, still share nothing where they lie in the rows' gaps.
+  // Their spans meet.  Pieces at one pitch (column blocks of a wider matrix), at multiples of one
+  // pitch (of every row of it and of every other one), or one piece against rows, still share nothing
+  // where they lie in the rows' gaps.  (Pitches whose common divisor leaves no room for both, such as
+  // 100 and 101 elements, are taken to meet: nothing that lies in one matrix has them.)
   if (a.rows == 1 && b.rows > 1) return share_bytes(b, a);
-  if (a.rows == 1 || (b.rows > 1 && a.pitch != b.pitch)) return true;
-  int64_t d = ((int64_t)b0 - (int64_t)a0) % a.pitch;   // b's place in a's row, 0 <= d < pitch
-  if (d < 0) d += a.pitch;
-  return d < a.width || d + b.width > a.pitch;
+  if (a.rows == 1) return true;
+  const int64_t pitch = b.rows == 1 ? a.pitch : std::gcd(a.pitch, b.pitch);
+  int64_t d = ((int64_t)b0 - (int64_t)a0) % pitch;   // b's place in a's row, 0 <= d < pitch
+  if (d < 0) d += pitch;
+  return d < a.width || d + b.width > pitch;
 }
 
 bool same(const Area& a, const Area& b) {

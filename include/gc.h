@@ -405,7 +405,8 @@ int gc_decompress_gathered(const gc_plan* plan, int32_t n_workers, const float* 
  * calls give the same bits.  The calls run on the current device, which the buffers must belong to,
  * and keep nothing between calls; a workspace belongs to one call at a time.  An output may be the
  * very same matrix (pointer and pitch) as an input where stated; any other shared byte between an
- * output and another buffer is an error.
+ * output and another buffer is an error (and so are two buffers of several rows in each other's gaps
+ * at pitches that are not multiples of a common one with room for a row of both).
  * Limits (GC_ERR_UNSUPPORTED beyond them): rows <= 2^25, cols and n_out <= 2^27, rows * pitch
  * <= 2^34, n_out * cols < 2^31, cols <= 32768 for the norm.
  * Errors: GC_ERR_INVALID_ARG (nothing launched), GC_ERR_UNSUPPORTED, GC_ERR_HIP.

@@ -133,3 +133,28 @@ def test_a_stream_of_another_device_is_refused():
     torch.cuda.synchronize()
     for k, t in vars(b).items():
         assert torch.equal(t.view(torch.uint8), before[k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("every", [2, 3])
+def test_column_blocks_of_all_rows_and_of_every_second_or_third_row(every):
+    """x in every row of a buffer, h and y beside it in every second or third row: pitches that
+    differ, and no shared byte."""
+    rows, cols = 5, 64
+    wide = torch.full((rows * every, 3 * cols + 5), 7.0, device="cuda")
+    x, h, y = wide[:rows, :cols], wide[::every, cols:2 * cols], wide[::every, 2 * cols + 5:]
+    x.copy_(torch.randn(rows, cols, generator=torch.Generator("cuda").manual_seed(1), device="cuda"))
+    want, untouched = torch.empty(rows, cols, device="cuda"), wide.clone()
+    gca.rmsnorm(x.contiguous(), y=want)
+    gca.rmsnorm(x, h=h, y=y)
+    assert torch.equal(h, x) and torch.equal(y, want)
+    gca.rmsnorm(y, y=x)                       # and the other way round
+    gca.rmsnorm(want, y=h)
+    assert torch.equal(x, h)
+    for t in (x, h, y):
+        t.fill_(0.0)
+    for t in (untouched[:rows, :cols], untouched[::every, cols:2 * cols],
+              untouched[::every, 2 * cols + 5:]):
+        t.fill_(0.0)
+    assert torch.equal(wide, untouched)
+    with pytest.raises(gca.GCError):
+        gca.rmsnorm(x, y=wide[::every, cols - 1:2 * cols - 1])
