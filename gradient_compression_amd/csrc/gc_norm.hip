@@ -133,15 +133,14 @@ struct GradRow {
 };
 
 // A worker (a wave or a block, as in the forward pass) takes the rows worker, worker + workers, ...
-// Its threads keep their columns' partial sums of dw in registers, and their weights and the next
-// row, loaded before the current one is reduced, where the registers last (up to 4 and up to 2
-// octets a thread).  A row is held as it was loaded and expanded twice: its floats would cost half
-// of the waves.
+// Its threads keep their columns' weights and partial sums of dw in registers, and with up to 2 octets
+// the next row, loaded before the current one is reduced.  A row is held as it was loaded and expanded
+// twice: its floats would cost half of the waves.
 template <int DT, int TPR, int NV, bool kStream>
 __global__ __launch_bounds__(block_threads<TPR>(), (backward_waves<TPR, NV>())) void k_rmsnorm_backward(NormGradArgs a) {
   typedef typename Elt<DT>::T T;
   constexpr int kRows = block_threads<TPR>() / TPR, kWavesN = TPR / 64;
-  constexpr bool kAhead = NV <= 2, kKeepW = NV <= 4;
+  constexpr bool kAhead = NV <= 2;
   __shared__ float s_part[2][kWavesN];
   __shared__ float s_dw[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * NV * 8 : 1];
   const int t = TPR == 64 ? lane_id() : threadIdx.x;
@@ -150,11 +149,9 @@ __global__ __launch_bounds__(block_threads<TPR>(), (backward_waves<TPR, NV>())) 
   const int cols = a.cols, octets = (cols + kActGroup - 1) / kActGroup * (kActGroup / 8);
   const bool has_res = a.dres.p != nullptr;
 
-  float dw[NV][8] = {}, w[kKeepW ? NV : 1][8];
-  if (kKeepW)
+  float dw[NV][8] = {}, w[NV][8];
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      load8_any(a.weight, a.weight_dtype, (t + v * TPR) * 8, cols, w[v]);
+  for (int v = 0; v < NV; ++v) load8_any(a.weight, a.weight_dtype, (t + v * TPR) * 8, cols, w[v]);
   auto load = [&](int64_t row, GradRow<DT, NV>& r) {
     const T* dy = static_cast<const T*>(a.dy.p) + row * a.dy.ld;
     const T* dres = static_cast<const T*>(a.dres.p) + row * a.dres.ld;
@@ -187,12 +184,11 @@ __global__ __launch_bounds__(block_threads<TPR>(), (backward_waves<TPR, NV>())) 
       float g[8], z[8];
       to_float8<DT>(cur.dy[v], g);
       decode8(cur.codes[v], exponent_scale(cur.exps[v]), z);
-      if (!kKeepW) load8_any(a.weight, a.weight_dtype, (t + v * TPR) * 8, cols, w[0]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[v][j] = fmaf(g[j], z[j], dw[v][j]);
         asm("" : "+v"(dw[v][j]));   // now, or g and z are kept for it until the row's end
-        s = fmaf(g[j] * w[kKeepW ? v : 0][j], z[j], s);
+        s = fmaf(g[j] * w[v][j], z[j], s);
       }
     }
     // the waves' sums alternate between two places, so that one meeting a row is enough
@@ -220,11 +216,10 @@ __global__ __launch_bounds__(block_threads<TPR>(), (backward_waves<TPR, NV>())) 
       float g[8], z[8], r[8];
       to_float8<DT>(cur.dy[v], g);
       decode8(cur.codes[v], exponent_scale(cur.exps[v]), z);
-      if (!kKeepW) load8_any(a.weight, a.weight_dtype, col, cols, w[0]);
       to_float8<DT>(cur.dres[v], r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        g[j] = cur.rstd * fmaf(-z[j], c, g[j] * w[kKeepW ? v : 0][j]) + r[j];
+        g[j] = cur.rstd * fmaf(-z[j], c, g[j] * w[v][j]) + r[j];
       }
       store8<DT>(dx, col, cols, g);
     }
