@@ -158,3 +158,43 @@ def test_column_blocks_of_all_rows_and_of_every_second_or_third_row(every):
     assert torch.equal(wide, untouched)
     with pytest.raises(gca.GCError):
         gca.rmsnorm(x, y=wide[::every, cols - 1:2 * cols - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,n_out,cols", [(70, 5, 33), (130, 100, 257), (300, 1000, 200), (200, 260, 3601)])
+def test_what_lies_between_the_rows_does_not_reach_the_results(rows, n_out, cols, dtype):
+    """Rows of every matrix in a buffer that is NaN between them; whole numbers, so sums are exact."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+
+    def matrix(width, pad, most):
+        wide = torch.full((rows, width + pad), float("nan"), dtype=dtype, device="cuda")
+        m = wide[:, :width]
+        m.copy_(torch.randint(-most, most + 1, (rows, width), generator=gen, device="cuda"))
+        return m
+
+    pitch, groups = gca.act_layout(cols)
+    codes = torch.randint(-20, 21, (rows, pitch), generator=gen, device="cuda", dtype=torch.int8)
+    codes[:, cols:] = 0
+    exps = torch.full((rows, groups), 127, dtype=torch.uint8, device="cuda")
+    for pad in (1, 8, 19):
+        dout = matrix(n_out, pad, 30)
+        dl = torch.empty(n_out, cols, device="cuda")
+        gca.act_weight_grad(dout, codes, exps, dl)
+        want = dout.float().t().contiguous() @ codes[:, :cols].float()
+        assert torch.equal(dl, want)
+        x, res, dres = (matrix(cols, pad, 9) for _ in range(3))
+        outs = [torch.empty(rows, cols, dtype=dtype, device="cuda") for _ in range(4)]
+        h, y, dx, dx2 = outs
+        h2, y2 = torch.empty_like(h), torch.empty_like(y)
+        c, e = torch.empty_like(codes), torch.empty_like(exps)
+        rstd, dw, dw2 = (torch.empty(n, device="cuda") for n in (rows, cols, cols))
+        gca.rmsnorm(x, residual=res, h=h, y=y, rstd=rstd, codes=c, exps=e)
+        gca.rmsnorm(x.contiguous(), residual=res.contiguous(), h=h2, y=y2)
+        gca.rmsnorm_backward(x, c, e, rstd, dx, dres=dres, dweight=dw)
+        gca.rmsnorm_backward(x.contiguous(), c, e, rstd, dx2, dres=dres.contiguous(), dweight=dw2)
+        for a, b in ((h, h2), (y, y2), (dx, dx2), (dw, dw2)):
+            assert torch.equal(a, b) and not torch.isnan(a).any()
+        c2, e2 = torch.empty_like(codes), torch.empty_like(exps)
+        gca.act_quant(x, c, e)
+        gca.act_quant(x.contiguous(), c2, e2)
+        assert torch.equal(c, c2) and torch.equal(e, e2) and not bool((e == 255).any())
