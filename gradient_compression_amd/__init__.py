@@ -666,7 +666,10 @@ _MASK64 = 2 ** 64 - 1
 def act_quant(x, codes, exps, stochastic: bool = False, seed: int = 0, step: int = 0,
               stream=None):
     """x into its 8-bit checkpoint: one power-of-two scale for 32 columns of a row, codes rounded
-    to nearest even or, with ``stochastic``, by the Philox stream of (seed, step)."""
+    to nearest even or, with ``stochastic``, by the Philox stream of (seed, step).  The draws are
+    those of seed, step (low 32 bits) and an element's place: give each matrix, a layer's or a
+    micro-batch's, a seed or a step of its own, or their rounding errors are alike and do not
+    average out."""
     dev = _device_of(x, "x")
     p, ld, rows, cols, code = _matrix(x, "x", dev)
     cp, ep = _checkpoint(codes, exps, rows, cols, dev)
@@ -691,7 +694,7 @@ def rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, h=None, y=None, rs
     """h = x + residual; rstd = 1 / sqrt(mean(h^2) + eps); z = h * rstd; y = z * weight, and z's
     8-bit checkpoint into (codes, exps).  ``h``, ``y``, ``rstd`` (float32[rows]) and the
     checkpoint are written where given (at least y or the checkpoint); h or y may be x or
-    residual itself."""
+    residual itself.  ``stochastic``, ``seed`` and ``step`` as in act_quant."""
     dev = _device_of(x, "x")
     xp, ld_x, rows, cols, code = _matrix(x, "x", dev)
     rp, ld_r = _like(residual, "residual", dev, x, "x")

@@ -392,15 +392,20 @@ int gc_decompress_gathered(const gc_plan* plan, int32_t n_workers, const float* 
  *   GC_ROUND_STOCHASTIC : code = sign(x) * (floor(a) + [u24 < (a - floor(a)) * 2^24]), u24 the top
  *         24 bits of word (i % 4) of the Philox4x32-10 block keyed (seed low 32 bits, seed high 32
  *         bits) at counter (i / 4 low, i / 4 high, step low 32, 0x54), i = row * pitch + column:
- *         the restored value's expectation is x;
+ *         the restored value's expectation is x, to 2^-24 of a step.  The draws are those of seed,
+ *         step and place alone, so two matrices written with the same seed and step are rounded
+ *         alike, and what was summed over them (micro-batches, layers) keeps the errors that it
+ *         would otherwise average out: give each matrix (a layer's, a micro-batch's) a seed or a
+ *         step of its own;
  *   a group that holds Inf or NaN, or A > 127 * 2^121: b = 255 and codes 0.
- * Restored value: code * 2^(b - 127), exact in fp32 and in bf16 (a group of b = 255 is NaN; other
- * bytes above 248 are not written and what they restore to is unspecified).  The
- * error is at most 2^(e-1) (nearest), below 2^e (stochastic); 2^e < A / 63.
+ * Restored value: code * 2^(b - 127), exact in fp32 and in bf16 (a group of b = 255 is NaN; bytes
+ * below 7 and from 249 to 254 are not written and what they restore to is unspecified).  The
+ * error is at most 2^(e-1) (nearest), below 2^e (stochastic); 2^e < A / 63 where e > -120.
  *
  * Matrices are row-major with unit column stride and a row pitch `ld` in elements (ld >= cols),
  * of a gc_dtype.  No alignment beyond the element's is required of them; 16-byte aligned rows
- * (pointer and pitch) are faster.  Rows or columns of 0 are allowed.  Sums are in fp32 (the norm's
+ * (pointer and pitch) are faster.  Rows or columns of 0 are allowed (without columns no output is
+ * written, rstd among them).  Sums are in fp32 (the norm's
  * square sum in double) in an order that depends on the sizes and types alone, so that repeated
  * calls give the same bits.  The calls run on the current device, which the buffers must belong to,
  * and keep nothing between calls; a workspace belongs to one call at a time.  An output may be the
