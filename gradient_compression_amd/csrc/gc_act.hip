@@ -3,10 +3,12 @@
 // Both are streams: s + 1.03 bytes an element (s the type's size) and about 6 operations, so HBM
 // bounds them.  A lane takes one octet (one 16-byte load of a 16-bit type); a group's largest
 // magnitude is found inside its quad of lanes, so nothing goes through LDS.  Measured on 8192 x 11008
-// bf16: written in 49 us (5.6 TB/s; a copy of 4 GiB reaches 5.0), read back in 45 us (6.1 TB/s; 48 us
-// without non-temporal stores, which the codes' writer does not use: they are read back soon, and
-// writing and reading 4096 x 4096 took 22.3 us with them and 20.2 without).  Stochastic rounding is
-// bound by its draws (two Philox blocks for 8 columns): 82 us.
+// bf16: written in 49 us (5.6 TB/s; a copy of 4 GiB reaches 5.0), read back in 43 us (6.3 TB/s; 48 us
+// without non-temporal stores).  The codes' writer does not use such stores, which keeps the codes in
+// the cache for a reader that follows at once and costs a writer alone: 8192 x 4096 written and read
+// 38 us against 41, 4096 x 4096 19.0 against 21.5; written only 22.0 against 19.5 and 10.0 against 10.6
+// (8192 x 11008: 49 us either way).  Stochastic rounding is bound by its draws (two Philox blocks for
+// 8 columns): 77 us.
 #include "gc_act_internal.h"
 
 #include "gc_act.h"

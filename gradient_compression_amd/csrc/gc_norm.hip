@@ -8,11 +8,15 @@
 //   t = dy * w;  c = mean(t * z);  dx = rstd * (t - z * c) + dres;  dw = sum over rows of dy * z.
 //
 // Both are streams (4 s + 1.03 and 3 s + 1.03 bytes an element), so HBM bounds them: a row stays
-// in registers between its sum and its outputs, everything is read once.  The square sum is in
+// in registers between its sum and its outputs (but for the backward pass of rows of more than 16384
+// columns), everything is read once.  The square sum is in
 // double because the codes next to a rounding border follow rstd's last bit (and so that no
 // finite row overflows); it costs one double operation an element, hidden under the loads.
-// Measured on 8192 x 4096 bf16: forward 55 us (5.5 TB/s; a copy of 4 GiB reaches 5.0; 58 us without
-// non-temporal stores), backward 54 us with the 4.8 us of its column sums (4.4 TB/s).
+// Measured on 8192 x 4096 bf16: forward 54 us (5.6 TB/s; a copy of 4 GiB reaches 5.0), with stochastic
+// codes 59; backward 47 us and 4.9 us of its column sums (4.5 TB/s).  fp32: forward 132 us (4.3 TB/s),
+// backward 94 (4.6).  Rows of more than 16384 columns do not fit a block's registers in the backward
+// pass: 181 (16-bit types) and 425 (fp32) values a thread go through scratch memory in every row, and
+// 2048 x 32768 takes 187 and 342 us (2.5 TB/s; 4096 x 16384 109 and 185 us, 4.4 and 4.7 TB/s).
 #include "gc_act_internal.h"
 
 #include "gc_act.h"
@@ -110,6 +114,9 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm(NormArgs a) {
       uint32_t e;
       const u2 q = encode8<kRandom>(h[v], (uint64_t)i * 2, a.round.seed_lo, a.round.seed_hi,
                                     a.round.step_lo, &e);
+      // non-temporal at any pitch: they are read in the backward pass (norm alone of 8192 x 4096 bf16
+      // into codes 20.3 us against 23.5, 31775 x 1056, whose rows are not whole blocks, 24.2 against
+      // 28.3; with y and h 55.5 against 55.9 and 61.4 against 62.5)
       __builtin_nontemporal_store(q, reinterpret_cast<u2*>(a.codes) + i);
       if ((octet & 3) == 0) a.exps[i >> 2] = (uint8_t)e;
     }
@@ -117,7 +124,8 @@ __global__ __launch_bounds__(block_threads<TPR>()) void k_rmsnorm(NormArgs a) {
 }
 
 // Waves of a SIMD that the backward pass's registers are held to: two blocks of 512 threads a CU as
-// long as that costs no more than a few spilled registers.
+// long as that costs no more than a few spilled registers (9 in 16-bit rows of 3 octets a thread, 12
+// and 19 in fp32 rows of 2 and 3).  Blocks of 1024 threads have 128 registers a thread in any case.
 template <int TPR, int NV>
 constexpr int backward_waves() {
   return TPR == 512 && NV <= 3 ? 4 : 1;
@@ -340,8 +348,10 @@ void by_columns_backward(int32_t cols, F&& f) {
 template <int DT>
 void backward(const NormGradArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)norm_grad_blocks(a.rows, a.cols);
-  // dy and dres of 32 MB each are not in a cache any more: non-temporal loads then take 41.9 us in
-  // place of 46.8 for 4096 x 4096 bf16 and a reader of dx, but 20.3 in place of 18.7 for 1024 x 4096
+  // dy and dres of 32 MB each are not in a cache any more: non-temporal loads then take 39.4 us in
+  // place of 44.6 for 4096 x 4096 bf16 and a reader of dx, 72.2 in place of 75.6 for 8192 x 4096, 36.2
+  // in place of 41.0 for 16384 x 1024, but 25.2 in place of 24.5 for 2048 x 4096.  In fp32 they gain
+  // nothing at 32 MB (27.7 us either way) and lose at 128 MB (8192 x 4096 95.8 us against 89.5).
   const bool stream = a.rows * a.cols * (int64_t)sizeof(typename Elt<DT>::T) >= (int64_t)32 << 20;
   by_columns_backward(a.cols, [&](auto tpr, auto nv) {
     if (stream)

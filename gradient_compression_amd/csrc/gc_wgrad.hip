@@ -9,11 +9,12 @@
 // Both operands have the summed dimension as their slow one, so they are staged in LDS as they lie
 // in memory, the codes restored on the way (once for a tile's 256 columns of dY), and read across
 // their rows by LDS's transposing reads.  Measured: 8192 x 11008 x 4096 bf16 in 0.67 to 0.77 ms (960 to
-// 1100 TFLOP/s; a library product of bf16 operands in this layout reaches 950 on that shape), 4096
-// x 4096 x 4096 in 0.13 to 0.15 ms.  The matrix cores are busy for 56 % of the cycles; LDS (no bank
-// conflicts) for 35 %; the clock is held at 1.8 to 1.9 GHz by the card's power, so that the energy
-// of a step sets its time more than its schedule does: tiles with more loads a product (256 x 128)
-// took 11 % longer, without any restoring a step took 7 % less.
+// 1100 TFLOP/s; added to what is there 0.73 ms; a library product of bf16 operands in this layout
+// reaches 950 on that shape), 4096 x 4096 x 4096 in 0.13 to 0.15 ms; fp16 in 1.23 and 0.22 ms, fp32 in
+// 1.95 and 0.33 (two and three products a value: 600 and 620, 380 and 420 TFLOP/s).  The matrix cores are busy
+// for 56 % of the cycles; LDS (no bank conflicts) for 35 %; the clock is held at 1.8 to 1.9 GHz by the
+// card's power, so that the energy of a step sets its time more than its schedule does: tiles with more
+// loads a product (256 x 128) took 11 % longer, without any restoring a step took 7 % less.
 #include <type_traits>
 
 #include "gc_act_internal.h"
@@ -405,10 +406,14 @@ int64_t tiles_of(int32_t n_out, int32_t cols, int t) {
 //   fp16        14     9 11     5  6  8    (32 rows, 2 parts)
 //   fp32        25    12 17     8 10 13    (32 rows, 3 parts)
 // A call costs 4 us besides, a join 4 us, 0.1 us a part and its bytes (written and read) at 6 TB/s, or
-// at 4 where the parts pass 100 MB.  Against every
-// other choice, measured: 512 rows of 1024 x 1024 bf16 take tiny tiles, 7.9 us (small 11.5, small in
-// 4 parts 19.3); 8192 rows of 2048 x 2048 large ones in 4 parts, 84 us (small 115, tiny 152); 4096 rows
-// of 512 x 512 tiny ones in 8 parts, 15.5 us (whole 33.6).
+// at 4 where the parts pass 100 MB.  Three shapes were measured against every other choice: 512 rows
+// of 1024 x 1024 bf16 take tiny tiles, 7.9 us (small 11.5, small in 4 parts 19.3); 8192 rows of 2048 x
+// 2048 large ones in 4 parts, 84 us (small 115, tiny 152); 4096 rows of 512 x 512 tiny ones in 8 parts,
+// 15.5 us (whole 33.6).  Estimates against measured times: 2048 rows of 2048 x 2048 bf16 33 and 33 us,
+// 8192 of 1024 x 1024 43 and 40, 1531 of 1025 x 1000 fp32 30 and 28, 4096 of 4096 x 4096 fp32 324 and
+// 326; large tiles on every CU for long, whose clock the card's power lowers, take more than estimated
+// in the 16-bit types: 4096 of 4096 x 4096 bf16 113 and 132, fp16 183 and 220, 8192 of 11008 x 4096
+// 657 and 700, 1079 and 1230.
 Shape shape_of(int64_t rows, int32_t n_out, int32_t cols, int dtype) {
   constexpr int kPerCU[3] = {1, 2, 3};
   constexpr double kStepTime[3][3][3] = {   // by type (kF32, kBF16, kF16), tile, workgroups on the CU
