@@ -43,7 +43,9 @@ EXPORTS = ("gc_plan_create", "gc_plan_destroy", "gc_plan_total_k", "gc_plan_layo
            "gc_clip_by_norm", "gc_clip_factors", "gc_plan_set_gradient_scale", "gc_layout",
            "gc_act_layout", "gc_act_quant", "gc_act_restore", "gc_rmsnorm",
            "gc_rmsnorm_backward_workspace", "gc_rmsnorm_backward",
-           "gc_act_weight_grad_workspace", "gc_act_weight_grad")
+           "gc_act_weight_grad_workspace", "gc_act_weight_grad",
+           "gc_gated_linear_workspace", "gc_gated_linear", "gc_gated_linear_backward_workspace",
+           "gc_gated_linear_backward", "gc_grad_norm_workspace", "gc_grad_norm", "gc_grad_clip")
 
 _libs: dict = {}
 
@@ -114,6 +116,15 @@ def lib(variant: str | None = None) -> ctypes.CDLL:
         "gc_act_weight_grad_workspace": [i64, i64, i64, i32, vp],
         "gc_act_weight_grad": [vp, i64, i32, i64, i64, i64, vp, vp, vp, i32, vp, ctypes.c_int, vp,
                                i64, vp],
+        "gc_gated_linear_workspace": [i64, i64, i64, i32, vp],
+        "gc_gated_linear": [vp, i64, i32, i64, i64, vp, i64, vp, i64, i64, i32, vp, i64, vp, i64, vp,
+                            i64, vp, i64, vp],
+        "gc_gated_linear_backward_workspace": [i64, i64, i64, i32, vp],
+        "gc_gated_linear_backward": [vp, i64, vp, i64, vp, i64, i32, i64, i64, i32, vp, i64, vp, i64,
+                                     vp, i64, vp, i64, i64, vp, i64, vp, i64, vp],
+        "gc_grad_norm_workspace": [vp, i32, vp],
+        "gc_grad_norm": [vp, vp, vp, i32, vp, vp, vp, i64, vp],
+        "gc_grad_clip": [vp, vp, vp, i32, vp, vp, f32, vp, vp, i64, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -784,9 +795,248 @@ def act_weight_grad(dy, codes, exps, dweight, col_scale=None, accumulate: bool =
     _types[4]((dweight,))
 
 
+# ------------------------------------------------------------ the gated feed-forward block
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _activation(name):
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
+    return code
+
+
+def _weight(t, name, like, like_name, n, cols, dev):
+    """(pointer, row pitch) of a weight of n x cols, of the type of another matrix."""
+    p, ld, rows, width, _ = _matrix(t, name, dev)
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
+    if t.dim() != 2 or rows != n or width != cols:
+        raise ValueError(f"{name} must be {n} x {cols}, got {tuple(t.shape)}")
+    return p, ld
+
+
+def _rows_like(t, name, dev, like, like_name, cols):
+    """(pointer, row pitch) of a matrix with the leading dimensions and the type of another, and
+    `cols` columns; NULL for None."""
+    if t is None:
+        return None, 0
+    p, ld, _, width, _ = _matrix(t, name, dev)
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
+    if width != cols or t.shape[:-1] != like.shape[:-1]:
+        raise ValueError(f"{name} must have the shape {(*like.shape[:-1], cols)}, got "
+                         f"{tuple(t.shape)}")
+    return p, ld
+
+
+@functools.lru_cache(maxsize=4096)
+def gated_linear_workspace(rows: int, n: int, cols: int, dtype) -> int:
+    """Bytes of workspace of a gated_linear call (host-only)."""
+    code = (_types or _load_types())[2].get(dtype, -1)
+    b = ctypes.c_int64()
+    _check(lib().gc_gated_linear_workspace(int(rows), int(n), int(cols), code, ctypes.byref(b)),
+           "gc_gated_linear_workspace")
+    return b.value
+
+
+def gated_linear(x, w_gate, w_up, h, gate=None, up=None, activation: str = "silu", workspace=None,
+                 stream=None):
+    """h = act(x @ w_gate.T) * (x @ w_up.T), in one kernel: the gated half of a feed-forward block.
+    The weights are n x cols (of any row pitch: two halves of one matrix, or two matrices), h is
+    x's leading dimensions by n.  ``gate`` and ``up``: written where given, the two products that
+    gated_linear_backward starts from.  ``activation``: "silu", "gelu" (of the normal distribution
+    function) or "gelu_tanh" (its approximation).  ``workspace``: a tensor of gated_linear_workspace
+    bytes; allocated for the call when None."""
+    dev = _device_of(x, "x")
+    p, ld, rows, cols, code = _matrix(x, "x", dev)
+    if not isinstance(w_gate, _types[1]) or w_gate.dim() != 2:
+        raise TypeError("w_gate must be a matrix of outputs x columns")
+    n = w_gate.size(0)
+    gp, ld_g = _weight(w_gate, "w_gate", x, "x", n, cols, dev)
+    up_, ld_u = _weight(w_up, "w_up", x, "x", n, cols, dev)
+    if h is None:
+        raise TypeError("h must be a torch tensor")
+    hp, ld_h = _rows_like(h, "h", dev, x, "x", n)
+    kg, ld_kg = _rows_like(gate, "gate", dev, x, "x", n)
+    ku, ld_ku = _rows_like(up, "up", dev, x, "x", n)
+    st = _raw_stream(stream, dev)
+    ws, ws_bytes, _keep = _workspace(workspace, gated_linear_workspace(rows, n, cols, x.dtype),
+                                     stream, dev)
+    _check(lib().gc_gated_linear(p, ld, code, rows, cols, gp, ld_g, up_, ld_u, n,
+                                 _activation(activation), hp, ld_h, kg, ld_kg, ku, ld_ku, ws,
+                                 ws_bytes, st), "gc_gated_linear")
+    _types[4]([t for t in (h, gate, up) if t is not None])
+
+
+@functools.lru_cache(maxsize=4096)
+def gated_linear_backward_workspace(rows: int, n: int, cols: int, dtype) -> int:
+    """Bytes of workspace of a gated_linear_backward call with dx (host-only)."""
+    code = (_types or _load_types())[2].get(dtype, -1)
+    b = ctypes.c_int64()
+    _check(lib().gc_gated_linear_backward_workspace(int(rows), int(n), int(cols), code,
+                                                    ctypes.byref(b)),
+           "gc_gated_linear_backward_workspace")
+    return b.value
+
+
+def gated_linear_backward(dh, gate, up, dgate, dup, w_gate=None, w_up=None, dx=None,
+                          activation: str = "silu", workspace=None, stream=None):
+    """The gated block's backward pass from its kept gate and up: dgate = dh * up * act'(gate),
+    dup = dh * act(gate), and, where given, dx = dgate @ w_gate + dup @ w_up.  dgate and dup may be
+    dh, gate or up themselves; they are what act_weight_grad forms the weights' gradients from.
+    ``workspace``: a tensor of gated_linear_backward_workspace bytes; allocated for the call when
+    None."""
+    dev = _device_of(dh, "dh")
+    p, ld, rows, n, code = _matrix(dh, "dh", dev)
+    for t, name in ((gate, "gate"), (up, "up"), (dgate, "dgate"), (dup, "dup")):
+        if t is None:
+            raise TypeError(f"{name} must be a torch tensor")
+    gp, ld_g = _like(gate, "gate", dev, dh, "dh")
+    up_, ld_u = _like(up, "up", dev, dh, "dh")
+    dgp, ld_dg = _like(dgate, "dgate", dev, dh, "dh")
+    dup_, ld_du = _like(dup, "dup", dev, dh, "dh")
+    wg = wu = xp = None
+    ld_wg = ld_wu = ld_x = cols = need = 0
+    if dx is not None:
+        if not isinstance(dx, _types[1]) or dx.dim() < 1:
+            raise TypeError("dx must be a matrix")
+        cols = dx.size(-1)
+        xp, ld_x = _rows_like(dx, "dx", dev, dh, "dh", cols)
+        wg, ld_wg = _weight(w_gate, "w_gate", dh, "dh", n, cols, dev)
+        wu, ld_wu = _weight(w_up, "w_up", dh, "dh", n, cols, dev)
+        need = gated_linear_backward_workspace(rows, n, cols, dh.dtype)
+    elif w_gate is not None or w_up is not None:
+        raise ValueError("w_gate and w_up go with dx")
+    st = _raw_stream(stream, dev)
+    ws, ws_bytes, _keep = _workspace(workspace, need, stream, dev)
+    _check(lib().gc_gated_linear_backward(p, ld, gp, ld_g, up_, ld_u, code, rows, n,
+                                          _activation(activation), dgp, ld_dg, dup_, ld_du, wg,
+                                          ld_wg, wu, ld_wu, cols, xp, ld_x, ws, ws_bytes, st),
+           "gc_gated_linear_backward")
+    _types[4]((dgate, dup) if dx is None else (dgate, dup, dx))
+
+
+# ------------------------------------------------------------ the gradients of many tensors
+def _tensors(ts, name, dev):
+    """(pointers, sizes, type codes) of contiguous tensors, as host arrays."""
+    Tensor, codes = _types[1], _types[2]
+    try:
+        ptrs = [t.data_ptr() for t in ts]
+        sizes = [t.numel() for t in ts]
+        kinds = [codes[t.dtype] for t in ts]
+        fine = all([t.is_contiguous() and t.get_device() == dev for t in ts])
+    except (AttributeError, KeyError, RuntimeError):
+        fine = False
+    if not fine:      # say which
+        for i, t in enumerate(ts):
+            if not isinstance(t, Tensor) or t.get_device() != dev:
+                _refuse_place(t, f"{name}[{i}]", dev)
+            if t.dtype not in codes:
+                raise TypeError(f"{name}[{i}] must be float32, bfloat16 or float16, got {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+        raise TypeError(f"{name} must be strided tensors")
+    return (np.array(ptrs, np.uint64), np.array(sizes, np.int64), np.array(kinds, np.int32))
+
+
+def _outputs(out, arrays, tensors, dev):
+    """(pointers, type codes, tensors) of what the tensors are scaled into: themselves, as many
+    tensors, or one tensor that they are laid into back to back."""
+    ptrs, sizes, kinds = arrays
+    if out is None:
+        return ptrs, kinds, tensors
+    if isinstance(out, _types[1]):
+        total = int(sizes.sum())
+        at, code = _columns(out, "out", total, dev)
+        step = out.element_size()
+        first = np.concatenate(([0], np.cumsum(sizes)[:-1])) if len(sizes) else sizes
+        return ((first * step).astype(np.uint64) + np.uint64(at or 0),
+                np.full(len(sizes), code, np.int32), (out,))
+    out = list(out)
+    got = _tensors(out, "out", dev)
+    if not np.array_equal(got[1], sizes):
+        raise ValueError("out must hold as many tensors, of the same sizes")
+    return got[0], got[2], out
+
+
+def _scalar(t, name, dev):
+    return _array(t, name, _types[0].float32, 1, dev)
+
+
+def _grad_norm(arrays, norm, norms, workspace, stream, dev):
+    ptrs, sizes, kinds = arrays
+    n, L = len(sizes), lib()
+    need = ctypes.c_int64()
+    _check(L.gc_grad_norm_workspace(_np_ptr(sizes), n, ctypes.byref(need)),
+           "gc_grad_norm_workspace")
+    ws, ws_bytes, _keep = _workspace(workspace, need.value, stream, dev)
+    _check(L.gc_grad_norm(_np_ptr(ptrs), _np_ptr(sizes), _np_ptr(kinds), n,
+                          _scalar(norm, "norm", dev),
+                          _array(norms, "norms", _types[0].float32, n, dev), ws, ws_bytes,
+                          _raw_stream(stream, dev)), "gc_grad_norm")
+    _types[4]((norm,) if norms is None else (norm, norms))
+
+
+def _grad_clip(arrays, tensors, max_norm, norm, out, factors, stream, dev):
+    ptrs, sizes, kinds = arrays
+    to, to_kinds, written = _outputs(out, arrays, tensors, dev)
+    f = 0 if factors is None else factors.numel()
+    _check(lib().gc_grad_clip(_np_ptr(ptrs), _np_ptr(sizes), _np_ptr(kinds), len(sizes),
+                              _np_ptr(to), _np_ptr(to_kinds), float(max_norm),
+                              _scalar(norm, "norm", dev),
+                              _array(factors, "factors", _types[0].float32, f, dev), f,
+                              _raw_stream(stream, dev)), "gc_grad_clip")
+    _types[4](list(written) if factors is None else [*written, factors])
+
+
+def grad_norm_workspace(sizes) -> int:
+    """Bytes of workspace of a grad_norm or clip_grad_norm call over tensors of these numbers of
+    elements (host-only)."""
+    a = np.ascontiguousarray(sizes, np.int64)
+    need = ctypes.c_int64()
+    _check(lib().gc_grad_norm_workspace(_np_ptr(a), a.size, ctypes.byref(need)),
+           "gc_grad_norm_workspace")
+    return need.value
+
+
+def grad_norm(tensors, norm, norms=None, workspace=None, stream=None):
+    """norm (float32, one element) = the l2 norm over all elements of all tensors (contiguous, float32,
+    bfloat16 or float16 in any mixture), summed in double; norms (float32, one for each tensor) =
+    each one's.  ``workspace``: a tensor of grad_norm_workspace bytes; allocated for the call when
+    None."""
+    dev = _device_of(norm, "norm")
+    tensors = list(tensors)
+    _grad_norm(_tensors(tensors, "tensors", dev), norm, norms, workspace, stream, dev)
+
+
+def grad_clip(tensors, max_norm: float, norm, out=None, factors=None, stream=None):
+    """Scale all tensors by f = max_norm / norm where norm (float32, one element, as grad_norm gives
+    it or joined with other workers' shares) is above max_norm and finite, else by 1.  ``out``: where
+    the result goes, rounded to its type: a list of as many tensors, or one tensor that takes them
+    back to back (the flat gradient); in place when None (and left alone where f is 1).  ``factors``
+    (float32): all set to f, for Plan.set_gradient_scale."""
+    dev = _device_of(norm, "norm")
+    tensors = list(tensors)
+    _grad_clip(_tensors(tensors, "tensors", dev), tensors, max_norm, norm, out, factors, stream, dev)
+
+
+def clip_grad_norm(tensors, max_norm: float, norm, out=None, norms=None, factors=None,
+                   workspace=None, stream=None):
+    """grad_norm, and grad_clip by it: the gradients of a whole model scaled so that their norm is at
+    most max_norm, in place or into ``out``."""
+    dev = _device_of(norm, "norm")
+    tensors = list(tensors)
+    arrays = _tensors(tensors, "tensors", dev)
+    _grad_norm(arrays, norm, norms, workspace, stream, dev)
+    _grad_clip(arrays, tensors, max_norm, norm, out, factors, stream, dev)
+
+
 __all__ = ["Plan", "GCError", "lib", "status_string", "copy_f32", "add_f32", "read_f32", "layout",
            "topk_ef_compress_noalloc", "EXPORTS", "act_layout", "act_quant", "act_restore",
            "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace", "act_weight_grad",
-           "act_weight_grad_workspace", "ACT_GROUP",
+           "act_weight_grad_workspace", "ACT_GROUP", "ACTIVATIONS", "gated_linear",
+           "gated_linear_workspace", "gated_linear_backward", "gated_linear_backward_workspace",
+           "grad_norm", "grad_norm_workspace", "grad_clip", "clip_grad_norm",
            "GC_MOMENTUM_MASK", "GC_DEBUG_FORCE_FALLBACK", "GC_DEBUG_NO_ESTIMATE", "GC_DEBUG_CHAIN", "MODE_SKIP",
            "MODE_CANDIDATES", "MODE_FULL", "MODE_RECAPTURED", "MODE_SMALL", "SMALL_SEGMENT"]

@@ -19,12 +19,13 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libgc.so")
-# The compressors, whose kernels follow the tile geometry, and the activation operators, whose
-# kernels do not (every library holds both).
+# The compressors, whose kernels follow the tile geometry, and the activation operators and those over
+# many tensors, whose kernels do not (every library holds all).
 TILED = [os.path.join(HERE, "csrc", f) for f in ("gc_pass.hip", "gc_topk.hip", "gc_codecs.hip",
                                                      "gc_scatter.hip", "gc_api.hip")]
-ACTIVATION = [os.path.join(HERE, "csrc", f) for f in ("gc_act.hip", "gc_norm.hip",
-                                                          "gc_wgrad.hip", "gc_act_api.hip")]
+ACTIVATION = [os.path.join(HERE, "csrc", f) for f in ("gc_act.hip", "gc_norm.hip", "gc_wgrad.hip",
+                                                          "gc_gated.hip", "gc_act_api.hip",
+                                                          "gc_grads.hip", "gc_grads_api.hip")]
 SOURCES = TILED + ACTIVATION
 ARCH = "gfx950"
 

@@ -100,6 +100,17 @@ int status(hipError_t e) { return e == hipSuccess ? GC_OK : GC_ERR_HIP; }
 
 gc::Mat mat(const void* p, int64_t ld) { return {const_cast<void*>(p), ld}; }
 
+bool valid_activation(int32_t a) {
+  return a == GC_ACT_SILU || a == GC_ACT_GELU || a == GC_ACT_GELU_TANH;
+}
+
+// Sizes of a gated block: rows x cols through two n x cols weights.
+int check_block(int64_t rows, int64_t n, int64_t cols) {
+  if (int rc = check_sizes(rows, cols)) return rc;
+  if (int rc = check_sizes(rows, n)) return rc;
+  return n * cols > kMostCodes ? GC_ERR_UNSUPPORTED : GC_OK;   // both at most 2^27
+}
+
 }  // namespace
 
 extern "C" {
@@ -286,6 +297,107 @@ int gc_act_weight_grad(const void* dy, int64_t ld_dy, int32_t dtype, int64_t row
   a.accumulate = accumulate != 0;
   a.ws = static_cast<float*>(workspace);
   return status(gc::launch_wgrad(a, static_cast<hipStream_t>(stream)));
+}
+
+int gc_gated_linear_workspace(int64_t rows, int64_t n, int64_t cols, int32_t dtype,
+                              int64_t* bytes) {
+  if (!bytes || !valid_dtype(dtype)) return GC_ERR_INVALID_ARG;
+  if (int rc = check_block(rows, n, cols)) return rc;
+  *bytes = gc::gated_workspace(rows, (int32_t)n, (int32_t)cols, dtype);
+  return GC_OK;
+}
+
+int gc_gated_linear(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t cols,
+                    const void* w_gate, int64_t ld_w_gate, const void* w_up, int64_t ld_w_up,
+                    int64_t n, int32_t activation, void* h, int64_t ld_h, void* gate,
+                    int64_t ld_gate, void* up, int64_t ld_up, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+  int64_t need = 0;
+  if (int rc = gc_gated_linear_workspace(rows, n, cols, dtype, &need)) return rc;
+  if (!valid_activation(activation)) return GC_ERR_INVALID_ARG;
+  if (rows == 0 || n == 0) return GC_OK;
+  if (workspace_bytes < need || (need && !workspace) || !aligned(workspace, 16) ||
+      !valid_matrix(x, ld_x, rows, cols, dtype) || !valid_matrix(w_gate, ld_w_gate, n, cols, dtype) ||
+      !valid_matrix(w_up, ld_w_up, n, cols, dtype) || !valid_matrix(h, ld_h, rows, n, dtype) ||
+      (gate && !valid_matrix(gate, ld_gate, rows, n, dtype)) ||
+      (up && !valid_matrix(up, ld_up, rows, n, dtype)))
+    return GC_ERR_INVALID_ARG;
+  if (clash({matrix(x, ld_x, rows, cols, dtype, false),
+             matrix(w_gate, ld_w_gate, n, cols, dtype, false),
+             matrix(w_up, ld_w_up, n, cols, dtype, false), matrix(h, ld_h, rows, n, dtype, true),
+             matrix(gate, ld_gate, rows, n, dtype, true), matrix(up, ld_up, rows, n, dtype, true),
+             flat(workspace, need, true)}, {}))
+    return GC_ERR_INVALID_ARG;
+  gc::GatedArgs a{};
+  a.dtype = dtype;
+  a.act = activation;
+  a.rows = rows;
+  a.n = (int32_t)n;
+  a.cols = (int32_t)cols;
+  a.x = mat(x, ld_x);
+  a.w_gate = mat(w_gate, ld_w_gate);
+  a.w_up = mat(w_up, ld_w_up);
+  a.h = mat(h, ld_h);
+  a.gate = mat(gate, ld_gate);
+  a.up = mat(up, ld_up);
+  a.ws = workspace;
+  return status(gc::launch_gated(a, static_cast<hipStream_t>(stream)));
+}
+
+int gc_gated_linear_backward_workspace(int64_t rows, int64_t n, int64_t cols, int32_t dtype,
+                                       int64_t* bytes) {
+  if (!bytes || !valid_dtype(dtype)) return GC_ERR_INVALID_ARG;
+  if (int rc = check_block(rows, n, cols)) return rc;
+  *bytes = gc::gated_grad_workspace(rows, (int32_t)n, (int32_t)cols, dtype);
+  return GC_OK;
+}
+
+int gc_gated_linear_backward(const void* dh, int64_t ld_dh, const void* gate, int64_t ld_gate,
+                             const void* up, int64_t ld_up, int32_t dtype, int64_t rows, int64_t n,
+                             int32_t activation, void* dgate, int64_t ld_dgate, void* dup,
+                             int64_t ld_dup, const void* w_gate, int64_t ld_w_gate,
+                             const void* w_up, int64_t ld_w_up, int64_t cols, void* dx,
+                             int64_t ld_dx, void* workspace, int64_t workspace_bytes,
+                             void* stream) {
+  if (!dx) {   // the stream alone: nothing of the product is looked at
+    cols = 0;
+    w_gate = w_up = nullptr;
+  }
+  int64_t need = 0;
+  if (int rc = gc_gated_linear_backward_workspace(rows, n, cols, dtype, &need)) return rc;
+  if (!valid_activation(activation)) return GC_ERR_INVALID_ARG;
+  if (rows == 0) return GC_OK;
+  if (workspace_bytes < need || (need && !workspace) || !aligned(workspace, 16) ||
+      !valid_matrix(dh, ld_dh, rows, n, dtype) || !valid_matrix(gate, ld_gate, rows, n, dtype) ||
+      !valid_matrix(up, ld_up, rows, n, dtype) || !valid_matrix(dgate, ld_dgate, rows, n, dtype) ||
+      !valid_matrix(dup, ld_dup, rows, n, dtype) ||
+      !valid_matrix(w_gate, ld_w_gate, n, cols, dtype) ||
+      !valid_matrix(w_up, ld_w_up, n, cols, dtype) || !valid_matrix(dx, ld_dx, rows, cols, dtype))
+    return GC_ERR_INVALID_ARG;
+  if (clash({matrix(dh, ld_dh, rows, n, dtype, false), matrix(gate, ld_gate, rows, n, dtype, false),
+             matrix(up, ld_up, rows, n, dtype, false), matrix(dgate, ld_dgate, rows, n, dtype, true),
+             matrix(dup, ld_dup, rows, n, dtype, true),
+             matrix(w_gate, ld_w_gate, n, cols, dtype, false),
+             matrix(w_up, ld_w_up, n, cols, dtype, false), matrix(dx, ld_dx, rows, cols, dtype, true),
+             flat(workspace, need, true)},
+            {{0, 3}, {1, 3}, {2, 3}, {0, 4}, {1, 4}, {2, 4}}))
+    return GC_ERR_INVALID_ARG;
+  gc::GatedGradArgs a{};
+  a.dtype = dtype;
+  a.act = activation;
+  a.rows = rows;
+  a.n = (int32_t)n;
+  a.cols = (int32_t)cols;
+  a.dh = mat(dh, ld_dh);
+  a.gate = mat(gate, ld_gate);
+  a.up = mat(up, ld_up);
+  a.dgate = mat(dgate, ld_dgate);
+  a.dup = mat(dup, ld_dup);
+  a.w_gate = mat(w_gate, ld_w_gate);
+  a.w_up = mat(w_up, ld_w_up);
+  a.dx = mat(dx, ld_dx);
+  a.ws = workspace;
+  return status(gc::launch_gated_backward(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

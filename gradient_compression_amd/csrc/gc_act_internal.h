@@ -69,6 +69,27 @@ struct WgradArgs {
   float* ws;                   // [splits][n_out][cols] where splits > 1
 };
 
+// Activations of a gated block, in the numbering of gc_activation.
+constexpr int kSilu = 0, kGelu = 1, kGeluTanh = 2;
+
+struct GatedArgs {
+  int32_t dtype, act;
+  int64_t rows;
+  int32_t n, cols;
+  Mat x, w_gate, w_up;         // rows x cols, n x cols
+  Mat h, gate, up;             // rows x n; gate, up: p may be null
+  void* ws;
+};
+
+struct GatedGradArgs {
+  int32_t dtype, act;
+  int64_t rows;
+  int32_t n, cols;
+  Mat dh, gate, up, dgate, dup;   // rows x n
+  Mat w_gate, w_up, dx;           // n x cols, rows x cols; dx: p may be null (then the weights too)
+  void* ws;
+};
+
 constexpr int64_t kNormMostCols = 32768;
 
 hipError_t launch_act_quant(const Mat& x, int dtype, int64_t rows, int32_t cols,
@@ -82,5 +103,10 @@ hipError_t launch_rmsnorm_backward(const NormGradArgs& a, hipStream_t st);
 // Parts into which a weight gradient's sum over the rows is split.
 int wgrad_splits(int64_t rows, int32_t n_out, int32_t cols, int dtype);
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t st);
+// Bytes of workspace.
+int64_t gated_workspace(int64_t rows, int32_t n, int32_t cols, int dtype);
+int64_t gated_grad_workspace(int64_t rows, int32_t n, int32_t cols, int dtype);
+hipError_t launch_gated(const GatedArgs& a, hipStream_t st);
+hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t st);
 
 }  // namespace gc

@@ -1,0 +1,217 @@
+// gc_grads.hip -- the l2 norm over many tensors of any of the types, and their scaling by one factor.
+//
+// Both are streams: the norm reads every tensor once, the scaling reads it again (part of it from the
+// 256 MB cache) and writes the result.  Squares and sums are in double, so that neither the range
+// of fp32 nor the length of the sum matters; the order of a sum depends on the tensors' sizes alone.
+#include "gc_grads.h"
+
+#include "gc_act_internal.h"
+
+#include "gc_act.h"
+
+namespace gc {
+namespace {
+
+constexpr int kThreadsGrad = 256;
+
+// First tensor of the launch whose chunks reach beyond c (a tensor of no chunks never does).
+template <typename Table>
+__device__ __forceinline__ int tensor_of(const Table& t, uint32_t c) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (t.first[mid + 1] > c)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ uint32_t chunk_of(uint32_t block, uint32_t chunks, uint32_t blocks) {
+  return (uint32_t)((uint64_t)block * chunks / blocks);
+}
+
+// Sum of squares of n elements from p on, this thread's share.
+template <int DT>
+__device__ __forceinline__ double squares(const typename Elt<DT>::T* p, int n) {
+  double s[4] = {};
+  int i = threadIdx.x * 8;
+  for (; i + 8 <= n; i += kThreadsGrad * 8) {
+    float v[8];
+    to_float8<DT>(load_raw<DT>(p + i), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j & 3] = fma((double)v[j], (double)v[j], s[j & 3]);
+  }
+  for (int j = i; j < n && j < i + 8; ++j) {
+    const double v = to_float(p[j]);
+    s[0] = fma(v, v, s[0]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__device__ __forceinline__ double block_sum(double v, double* tmp) {
+  v = wave_sum(v);
+  if (lane_id() == 0) tmp[wave_id()] = v;
+  __syncthreads();
+  const double r = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+  __syncthreads();
+  return r;
+}
+
+__global__ __launch_bounds__(kThreadsGrad) void k_grad_squares(NormTable t, double* sums,
+                                                               GradSums* of, uint32_t base) {
+  __shared__ double s_tmp[kThreadsGrad / 64];
+  const uint32_t b = blockIdx.x, chunks = t.first[t.n];
+  const uint32_t from = chunk_of(b, chunks, t.blocks), to = chunk_of(b + 1, chunks, t.blocks);
+  int at = tensor_of(t, from);
+  // the slots before this block's first one that are nobody's
+  if (b == 0)
+    for (int i = threadIdx.x; i < at; i += kThreadsGrad) sums[i] = 0.0;
+  if (from == to && threadIdx.x == 0) sums[b + at] = 0.0;   // a launch without chunks
+  uint32_t c = from;
+  while (c < to) {
+    const uint32_t first = t.first[at], next = t.first[at + 1], end = next < to ? next : to;
+    const uint32_t info = t.tail[at];
+    double s = 0.0;
+    for (; c < end; ++c) {
+      const int n = c + 1 == next ? (int)(info & 0xFFFFu) : (int)kGradChunk;
+      const int64_t off = (int64_t)(c - first) * kGradChunk;
+      switch ((info >> 16) & 3) {
+        case kF32: s += squares<kF32>(static_cast<const float*>(t.p[at]) + off, n); break;
+        case kBF16: s += squares<kBF16>(static_cast<const __bf16*>(t.p[at]) + off, n); break;
+        default: s += squares<kF16>(static_cast<const _Float16*>(t.p[at]) + off, n);
+      }
+    }
+    s = block_sum(s, s_tmp);
+    if (threadIdx.x == 0) sums[b + at] = s;
+    if (c < to) ++at;
+  }
+  // and those up to the next block's first one
+  const int64_t stop = b + 1 < t.blocks ? (int64_t)b + 1 + tensor_of(t, to) : (int64_t)t.blocks + t.n;
+  for (int64_t i = (int64_t)b + at + 1 + threadIdx.x; i < stop; i += kThreadsGrad) sums[i] = 0.0;
+  if (b == 0)
+    for (int i = threadIdx.x; i < t.n; i += kThreadsGrad) {
+      const uint32_t c0 = t.first[i], c1 = t.first[i + 1];
+      GradSums g = {base, 0};
+      if (c1 > c0) {   // chunk c is block ceil((c + 1) * blocks / chunks) - 1's
+        const uint32_t b0 = (uint32_t)((((uint64_t)c0 + 1) * t.blocks + chunks - 1) / chunks) - 1;
+        const uint32_t b1 = (uint32_t)(((uint64_t)c1 * t.blocks + chunks - 1) / chunks) - 1;
+        g = {base + b0 + (uint32_t)i, b1 - b0 + 1};
+      }
+      of[i] = g;
+    }
+}
+
+// Block 0: the norm of all; the others: a tensor a wave.
+__global__ __launch_bounds__(kThreadsGrad) void k_grad_roots(const double* sums, uint32_t total,
+                                                             const GradSums* of, int32_t n,
+                                                             float* norm, float* norms) {
+  __shared__ double s_tmp[kThreadsGrad / 64];
+  double s = 0.0;
+  if (blockIdx.x == 0) {
+    for (uint32_t i = threadIdx.x; i < total; i += kThreadsGrad) s += sums[i];
+    s = block_sum(s, s_tmp);
+    if (threadIdx.x == 0) *norm = (float)sqrt(s);
+    return;
+  }
+  const int64_t t = (int64_t)(blockIdx.x - 1) * (kThreadsGrad / 64) + wave_id();
+  if (t >= n) return;
+  const GradSums g = of[t];
+  for (uint32_t i = lane_id(); i < g.count; i += 64) s += sums[g.first + i];
+  s = wave_sum(s);
+  if (lane_id() == 0) norms[t] = (float)sqrt(s);
+}
+
+// 1 where the norm is not above the limit, and where it is Inf or NaN (nothing sensible to scale by).
+__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+  return norm > max_norm && norm <= 3.402823466e38f ? max_norm / norm : 1.0f;
+}
+
+template <int DI, int DO>
+__device__ __forceinline__ void scale(const typename Elt<DI>::T* p, typename Elt<DO>::T* out, int n,
+                                      float f) {
+  for (int i = threadIdx.x * 8; i < n; i += kThreadsGrad * 8) {
+    float v[8];
+    if (i + 8 <= n)
+      to_float8<DI>(load_raw<DI>(p + i), v);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = i + j < n ? to_float(p[i + j]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f;
+    store8<DO>(out, i, n, v);
+  }
+}
+
+template <int DI>
+__device__ __forceinline__ void scale(const void* p, int64_t off, void* out, int dtype, int n,
+                                      float f) {
+  typedef const typename Elt<DI>::T* P;
+  if (dtype == kF32)
+    scale<DI, kF32>(static_cast<P>(p) + off, static_cast<float*>(out) + off, n, f);
+  else if (dtype == kBF16)
+    scale<DI, kBF16>(static_cast<P>(p) + off, static_cast<__bf16*>(out) + off, n, f);
+  else
+    scale<DI, kF16>(static_cast<P>(p) + off, static_cast<_Float16*>(out) + off, n, f);
+}
+
+__global__ __launch_bounds__(kThreadsGrad) void k_grad_clip(ClipTable t, float max_norm,
+                                                            const float* norm) {
+  const float f = clip_factor(*norm, max_norm);
+  const uint32_t chunks = t.first[t.n];
+  const uint32_t from = chunk_of(blockIdx.x, chunks, t.blocks);
+  const uint32_t to = chunk_of(blockIdx.x + 1, chunks, t.blocks);
+  int at = tensor_of(t, from);
+  for (uint32_t c = from; c < to; ++c) {
+    while (c >= t.first[at + 1]) ++at;
+    const uint32_t info = t.tail[at];
+    if (f == 1.0f && (info >> 20 & 1)) continue;   // it is where it belongs already
+    const int n = c + 1 == t.first[at + 1] ? (int)(info & 0xFFFFu) : (int)kGradChunk;
+    const int64_t off = (int64_t)(c - t.first[at]) * kGradChunk;
+    const int dtype = (info >> 18) & 3;
+    switch ((info >> 16) & 3) {
+      case kF32: scale<kF32>(t.p[at], off, t.out[at], dtype, n, f); break;
+      case kBF16: scale<kBF16>(t.p[at], off, t.out[at], dtype, n, f); break;
+      default: scale<kF16>(t.p[at], off, t.out[at], dtype, n, f);
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreadsGrad) void k_grad_factors(float max_norm, const float* norm,
+                                                               float* factors, int64_t n) {
+  const float f = clip_factor(*norm, max_norm);
+  for (int64_t i = (int64_t)blockIdx.x * kThreadsGrad + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * kThreadsGrad)
+    factors[i] = f;
+}
+
+}  // namespace
+
+hipError_t launch_grad_squares(const NormTable& t, double* sums, GradSums* of, uint32_t base,
+                               hipStream_t st) {
+  k_grad_squares<<<t.blocks, kThreadsGrad, 0, st>>>(t, sums, of, base);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_roots(const double* sums, uint32_t total, const GradSums* of, int32_t n,
+                             float* norm, float* norms, hipStream_t st) {
+  const unsigned grid = 1 + (norms ? blocks_for(n, kThreadsGrad / 64) : 0);
+  k_grad_roots<<<grid, kThreadsGrad, 0, st>>>(sums, total, of, n, norm, norms);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const ClipTable& t, float max_norm, const float* norm, hipStream_t st) {
+  k_grad_clip<<<t.blocks, kThreadsGrad, 0, st>>>(t, max_norm, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_factors(float max_norm, const float* norm, float* factors, int64_t n,
+                               hipStream_t st) {
+  const int64_t blocks = (n + kThreadsGrad - 1) / kThreadsGrad;
+  k_grad_factors<<<(unsigned)(blocks < 1024 ? blocks : 1024), kThreadsGrad, 0, st>>>(max_norm, norm,
+                                                                                     factors, n);
+  return hipGetLastError();
+}
+
+}  // namespace gc

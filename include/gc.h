@@ -489,6 +489,87 @@ int gc_act_weight_grad(const void* dy, int64_t ld_dy, int32_t dtype, int64_t row
                        const void* col_scale, int32_t scale_dtype, float* dweight, int accumulate,
                        void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * The gated feed-forward block behind a norm, in one kernel: x (rows x cols) through two weights of n
+ * outputs each (n x cols, a row an output), the gate's activation and the product:
+ *   G = x w_gate^T;  U = x w_up^T  (fp32 sums);  h = round(act(G) * U) to dtype, one rounding;
+ *   gate = round(G);  up = round(U)  (what the backward pass starts from; either may be NULL)
+ * with act(g) = g / (1 + exp(-g)) (GC_ACT_SILU), g * Phi(g) with the normal distribution function Phi
+ * (GC_ACT_GELU), or g / (1 + exp(-2 sqrt(2 / pi) (g + 0.044715 g^3))) (GC_ACT_GELU_TANH), in fp32.
+ * Everything shares dtype.  Products of bf16 and fp16 are exact; as in gc_act_weight_grad, values,
+ * products and sums below 2^-126 in magnitude may count as 0.  cols = 0 gives zeros.
+ * x is the y of a gc_rmsnorm; the weights' gradients are gc_act_weight_grad's of dgate and dup, with
+ * that norm's checkpoint.
+ *   workspace : 16-byte aligned, of at least gc_gated_linear_workspace bytes (may be NULL where that is
+ *               0).
+ * Limits beyond the matrices' (GC_ERR_UNSUPPORTED): n * cols <= 2^34.
+ */
+typedef enum { GC_ACT_SILU = 0, GC_ACT_GELU = 1, GC_ACT_GELU_TANH = 2 } gc_activation;
+
+int gc_gated_linear_workspace(int64_t rows, int64_t n, int64_t cols, int32_t dtype,
+                              int64_t* bytes /* host */);
+int gc_gated_linear(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t cols,
+                    const void* w_gate, int64_t ld_w_gate, const void* w_up, int64_t ld_w_up,
+                    int64_t n, int32_t activation, void* h, int64_t ld_h, void* gate,
+                    int64_t ld_gate, void* up, int64_t ld_up, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/*
+ * The block's backward pass from the kept gate and up:
+ *   dgate = round(dh * up * act'(gate));  dup = round(dh * act(gate))  to dtype;
+ *   dx = round(dgate w_gate + dup w_up) of dgate and dup as they are stored (fp32 sums).
+ *   dgate, dup : may each be dh, gate or up itself (not both the same).
+ *   dx         : may be NULL; then only dgate and dup are formed, and cols, the weights and the
+ *                workspace are not looked at.
+ *   workspace  : 16-byte aligned, of at least gc_gated_linear_backward_workspace bytes (may be NULL
+ *                where that is 0).
+ * n = 0 gives dx = 0.
+ */
+int gc_gated_linear_backward_workspace(int64_t rows, int64_t n, int64_t cols, int32_t dtype,
+                                       int64_t* bytes /* host */);
+int gc_gated_linear_backward(const void* dh, int64_t ld_dh, const void* gate, int64_t ld_gate,
+                             const void* up, int64_t ld_up, int32_t dtype, int64_t rows, int64_t n,
+                             int32_t activation, void* dgate, int64_t ld_dgate, void* dup,
+                             int64_t ld_dup, const void* w_gate, int64_t ld_w_gate,
+                             const void* w_up, int64_t ld_w_up, int64_t cols, void* dx,
+                             int64_t ld_dx, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The gradients of all tensors of a model, of any of the types, clipped by their global norm and laid
+ * into the flat fp32 gradient (or scaled where they lie).  gc_clip_by_norm does so per segment of a
+ * gradient that is flat already.
+ *
+ * n tensors, given by host arrays that are read during the call: tensors[t] (device pointer, aligned
+ * to its element; of contiguous elements), sizes[t] elements (0 is allowed; the pointer may be NULL
+ * then), dtypes[t] a gc_dtype.  Squares and sums are in double, in an order that depends on the sizes
+ * alone.  A captured call holds the pointers it was given.
+ * Limits (GC_ERR_UNSUPPORTED beyond them): n <= 2^20, 2^44 elements in all.
+ * Errors: GC_ERR_INVALID_ARG (nothing launched), GC_ERR_UNSUPPORTED, GC_ERR_OOM (host memory),
+ * GC_ERR_HIP.
+ *
+ * gc_grad_norm:
+ *   norm = fl32(sqrt(sum over all tensors and elements g^2));  norms[t] = the same of tensor t
+ *   norm      : device float[1]; 0 for no elements; Inf or NaN where an element is, and Inf above fp32's
+ *               range.  norms: device float[n], or NULL.
+ *   workspace : 16-byte aligned, of at least gc_grad_norm_workspace bytes.
+ * gc_grad_clip, with the norm of gc_grad_norm (or one that other workers' shares were joined to):
+ *   f = fl32(max_norm / norm) where norm > max_norm and norm is finite, else 1;
+ *   out[t][i] = round(fl32(f * tensors[t][i])) to out_dtypes[t];  factors[j] = f
+ *   out       : out[t] may be tensors[t] itself (of the same type; nothing is written there where f is
+ *               1), else it shares no byte with any tensor or other output.
+ *   max_norm  : >= 0, or Inf.  norm: device float[1], read only.
+ *   factors   : device float[n_factors], or NULL: what gc_plan_set_gradient_scale takes, for a gradient
+ *               that is flat already (n = 0 then).
+ */
+int gc_grad_norm_workspace(const int64_t* sizes /* host */, int32_t n, int64_t* bytes /* host */);
+int gc_grad_norm(const void* const* tensors /* host */, const int64_t* sizes /* host */,
+                 const int32_t* dtypes /* host */, int32_t n, float* norm, float* norms,
+                 void* workspace, int64_t workspace_bytes, void* stream);
+int gc_grad_clip(const void* const* tensors /* host */, const int64_t* sizes /* host */,
+                 const int32_t* dtypes /* host */, int32_t n, void* const* out /* host */,
+                 const int32_t* out_dtypes /* host */, float max_norm, const float* norm,
+                 float* factors, int64_t n_factors, void* stream);
+
 /* Forget the threshold estimates (of Top-k calls and the capture floor of threshold calls):
  * the next call runs as on a fresh plan. */
 int gc_plan_reset_estimate(gc_plan* plan, void* stream);
