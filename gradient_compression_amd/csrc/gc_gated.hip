@@ -145,6 +145,48 @@ __device__ __forceinline__ void multiply(const u4& w, const u4& x, f16v& acc) {
   }
 }
 
+// Rounds and stores a wave's products, of the forward pass after the activation.
+template <int DT, bool BACK, typename C, int ACT>
+__device__ __forceinline__ void finish(const Product& g, const f16v (&acc)[C::kFM][C::kFN],
+                                       int64_t m0, int n0, int wm, int wn) {
+  typedef typename Elt<DT>::T T;
+  const int half = lane_id() >> 5, in = lane_id() & 31;
+#pragma unroll
+  for (int i = 0; i < C::kFM; ++i) {
+    const int64_t row = m0 + wm + 32 * i + in;
+    if (row >= g.rows) continue;
+    auto put = [&](const Mat& m, int col, const float (&v)[8]) {
+      store8<DT>(static_cast<T*>(m.p) + row * m.ld, col, g.n, v);
+    };
+#pragma unroll
+    for (int j = 0; j < C::kFN; j += BACK ? 1 : 2)
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int col = n0 + (BACK ? wn + 32 * j : wn / 2 + 16 * j) + 16 * half + 8 * o;
+        if (col >= g.n) continue;
+        float v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = acc[i][j][8 * o + r];
+        if constexpr (BACK) {
+          put(g.out[0], col, v);
+        } else {
+          float u[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) u[r] = acc[i][j + 1][8 * o + r];
+          if (g.out[1].p) put(g.out[1], col, v);
+          if (g.out[2].p) put(g.out[2], col, u);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            float act, slope;
+            activate<ACT>(v[r], &act, &slope);
+            v[r] = act * u[r];
+          }
+          put(g.out[0], col, v);
+        }
+      }
+  }
+}
+
 template <int DT, bool BACK, typename C, int ACT>
 __global__ __launch_bounds__(C::kThreads) void k_product(Product g) {
   typedef typename Elt<DT>::T T;
@@ -252,44 +294,234 @@ __global__ __launch_bounds__(C::kThreads) void k_product(Product g) {
     nxt = t;
   }
 
+  finish<DT, BACK, C, ACT>(g, acc, m0, n0, wm, wn);
+}
+
+// ------------------------------------------------------------------ whole pieces: loaded into LDS directly
+// The same product where every row of an operand starts on 16 bytes and holds whole 16-byte pieces:
+// the loads write LDS themselves, a wave 1024 bytes of a stage at a time, in the order of the lanes; so
+// what a lane loads is what belongs into its place, and the places of a row's pieces are permuted as
+// above without a gap between rows.
+__device__ const u4 g_zeros = {0, 0, 0, 0};
+
+typedef __attribute__((address_space(1))) const void global_void;
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <int DT, bool BACK, int BM, int BN, int WM, int WN>
+struct DirectTile : Tile<DT, BACK, BM, BN, WM, WN> {
+  typedef Tile<DT, BACK, BM, BN, WM, WN> Base;
+  // pieces of a row of the second operand's stage
+  static constexpr int kPiecesB = BACK ? BN / Base::kElts : kRowChunks;
+  static constexpr int kPitchB = kPiecesB * kChunk;
+  static constexpr int kBytesB = (BACK ? Base::kBK : BN) * kPitchB, kStage = Base::kBytesA + kBytesB;
+  static constexpr int kRowsA = Base::kThreads / kRowChunks, kRowsB = Base::kThreads / kPiecesB;
+};
+
+// Where the 64-byte block b of row r lies in a row of the second operand (backward): the four rows of a
+// transposing read (fp32: the two halves of a wave, four rows apart) in different banks.
+template <int DT>
+__device__ __forceinline__ int block_at(int r, int b) {
+  return DT == kF32 ? b ^ ((r >> 1) & 2) : b ^ (r & 3);
+}
+
+template <int DT, bool BACK, typename C, int ACT>
+__global__ __launch_bounds__(C::kThreads, 2) void k_product_direct(Product g) {
+  typedef typename Elt<DT>::T T;
+  constexpr int E = C::kElts;
+  __shared__ __align__(16) char s_mem[2 * C::kStage];
+  const int tiles_m = (int)((g.rows + C::kBM - 1) / C::kBM);
+  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * C::kBM;
+  const int n0 = (int)(blockIdx.x / tiles_m) * C::kCols;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
+  const int wm = wave / C::kWN * (C::kFM * 32), wn = wave % C::kWN * (C::kFN * 32);
+  const int steps_seg = (g.depth + C::kBK - 1) / C::kBK, steps = BACK ? 2 * steps_seg : steps_seg;
+
+  // This thread's piece of every item: A's row p * kRowsA + ra, piece ca of the step; B's likewise.
+  const int ra = threadIdx.x / kRowChunks, ca = (threadIdx.x % kRowChunks) ^ ((ra >> 1) & 7);
+  const int rb = threadIdx.x / C::kPiecesB, sb = threadIdx.x % C::kPiecesB;
+  const int cb = BACK ? block_at<DT>(rb, sb >> 2) * 4 + (sb & 3) : sb ^ ((rb >> 1) & 7);
+  // The place of the next step to be fetched, the same in all lanes, and from it the byte offset of each
+  // item's row (rows past the last one read it, columns past the last one the tile's first; what they
+  // add up is not stored).
+  const char *pa, *pb[2];
+  int64_t next_b;
+  uint32_t off_a[C::kItemsA], off_b[C::kItemsB];
+  int left;              // of the segment's sum, from the next step on
+  auto start = [&](int seg) {
+    const Mat& a = g.a[seg];
+    left = g.depth;
+    pa = static_cast<const char*>(a.p) + m0 * a.ld * (int64_t)sizeof(T);
+    if (BACK) {
+      pb[0] = static_cast<const char*>(g.b[seg].p) + n0 * (int64_t)sizeof(T);
+      next_b = C::kBK * g.b[seg].ld * (int64_t)sizeof(T);
+    } else {
+      // a wave loads 8 rows at a time, of one of the weights: always the same or each in turn
+      const int w = C::kRowsB == 64 ? (wave >> 2) & 1 : 0;
+      pb[0] = static_cast<const char*>(g.b[w].p) + n0 * g.b[w].ld * (int64_t)sizeof(T);
+      pb[1] = static_cast<const char*>(g.b[1].p) + n0 * g.b[1].ld * (int64_t)sizeof(T);
+      next_b = kRowBytes;
+    }
 #pragma unroll
-  for (int i = 0; i < C::kFM; ++i) {
-    const int64_t row = m0 + wm + 32 * i + in;
-    if (row >= g.rows) continue;
-    auto put = [&](const Mat& m, int col, const float (&v)[8]) {
-      store8<DT>(static_cast<T*>(m.p) + row * m.ld, col, g.n, v);
-    };
+    for (int p = 0; p < C::kItemsA; ++p)
+      off_a[p] = (uint32_t)((min(m0 + p * C::kRowsA + ra, g.rows - 1) - m0) * a.ld *
+                            (int64_t)sizeof(T)) + ca * kChunk;
 #pragma unroll
-    for (int j = 0; j < C::kFN; j += BACK ? 1 : 2)
+    for (int p = 0; p < C::kItemsB; ++p) {
+      const int r = p * C::kRowsB + rb;
+      const int64_t pitch = g.b[BACK ? seg : (r >> 5) & 1].ld * (int64_t)sizeof(T);
+      if (BACK)
+        off_b[p] = (uint32_t)(r * pitch) + (n0 + cb * E < g.n ? cb * kChunk : 0);
+      else
+        off_b[p] = (uint32_t)((min(n0 + (r >> 6) * 32 + column_of(r & 31), g.n - 1) - n0) * pitch) +
+                   cb * kChunk;
+    }
+  };
+  auto item = [&](char* stage, const char* src, int p) {
+    __builtin_amdgcn_global_load_lds(
+        (global_void*)src, (lds_void*)(stage + wave * (64 * kChunk) + p * C::kThreads * kChunk),
+        kChunk, 0, 0);
+  };
+  auto from_b = [&](int p) { return pb[BACK || C::kRowsB == 64 ? 0 : p & 1] + off_b[p]; };
+  auto advance = [&] {
+    pa += kRowBytes;
+    pb[0] += next_b;
+    if (!BACK) pb[1] += next_b;
+    left -= C::kBK;
+  };
+  // The next step into a stage: one that is whole, and any; pieces behind the sum's end come from zeros.
+  auto fetch_whole = [&](char* stage) {
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int col = n0 + (BACK ? wn + 32 * j : wn / 2 + 16 * j) + 16 * half + 8 * o;
-        if (col >= g.n) continue;
-        float v[8];
+    for (int p = 0; p < C::kItemsA; ++p) item(stage, pa + off_a[p], p);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = acc[i][j][8 * o + r];
-        if constexpr (BACK) {
-          put(g.out[0], col, v);
-        } else {
-          float u[8];
+    for (int p = 0; p < C::kItemsB; ++p) item(stage, from_b(p), C::kItemsA + p);
+    advance();
+  };
+  auto fetch = [&](char* stage) {
+    if (BACK && left <= 0) start(1);
+    const char* none = reinterpret_cast<const char*>(&g_zeros);
 #pragma unroll
-          for (int r = 0; r < 8; ++r) u[r] = acc[i][j + 1][8 * o + r];
-          if (g.out[1].p) put(g.out[1], col, v);
-          if (g.out[2].p) put(g.out[2], col, u);
+    for (int p = 0; p < C::kItemsA; ++p) item(stage, ca * E < left ? pa + off_a[p] : none, p);
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            float act, slope;
-            activate<ACT>(v[r], &act, &slope);
-            v[r] = act * u[r];
-          }
-          put(g.out[0], col, v);
-        }
+    for (int p = 0; p < C::kItemsB; ++p)
+      item(stage, (BACK ? p * C::kRowsB + rb : cb * E) < left ? from_b(p) : none, C::kItemsA + p);
+    advance();
+  };
+
+  const int half = lane >> 5, in = lane & 31;
+  auto read_a = [&](const char* stage, int s, u4 (&f)[C::kFM]) {
+#pragma unroll
+    for (int i = 0; i < C::kFM; ++i)
+      f[i] = *reinterpret_cast<const u4*>(stage + piece_at(wm + 32 * i + in, 2 * s + half));
+  };
+  auto read_b = [&](const char* stage, int s, u4 (&f)[C::kFN]) {
+    const char* q = stage + C::kBytesA;
+#pragma unroll
+    for (int j = 0; j < C::kFN; ++j) {
+      if constexpr (!BACK) {
+        f[j] = *reinterpret_cast<const u4*>(q + piece_at(wn + 32 * j + in, 2 * s + half));
+      } else if constexpr (DT == kF32) {
+        const int r = (2 * s + half) * E, c = (wn + 32 * j) * 4 + column_of(in) * 4;
+        const char* t = q + r * C::kPitchB + block_at<DT>(r, c >> 6) * 64 + (c & 63);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f[j][e] = *reinterpret_cast<const uint32_t*>(t + e * C::kPitchB);
+      } else {
+        const int group = 4 * ((lane >> 4) & 1) + (lane & 3), r4 = (lane & 15) >> 2;
+        const char* t = q + ((2 * s + half) * E + r4) * C::kPitchB +
+                        block_at<DT>(r4, (wn + 32 * j) >> 5) * 64 +
+                        (16 * (group & 1) + 4 * (group >> 1)) * 2;
+        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)t);
+        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(t + 4 * C::kPitchB));
+        f[j] = __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
+    }
+  };
+
+  constexpr int kItems = C::kItemsA + C::kItemsB, kSlices = kRowChunks / 2;
+  static_assert(BACK || C::kRowsB == 64 || C::kRowsB == 32, "an item's rows of a wave are of one weight");
+  f16v acc[C::kFM][C::kFN] = {};
+  char *cur = s_mem, *nxt = s_mem + C::kStage;
+  u4 fa[C::kFM], fb[C::kFN];
+  if (steps) {
+    start(0);
+    fetch(cur);
+    asm volatile("" ::: "memory");
+    if (steps > 1) {
+      fetch(nxt);
+      // the first stage's loads are done when at most the second's are left
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kItems) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    read_a(cur, 0, fa);
+    read_b(cur, 0, fb);
   }
+  // One step: each slice is multiplied while the operands of the next are read.  Before the last one all
+  // waves meet: the next stage has arrived then and nobody reads this one any more, so that the step
+  // after the next goes there.
+  int step = 0;
+  auto multiply_step = [&](auto whole) {
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) {
+      u4 na[C::kFM], nb[C::kFN];
+      if (s + 1 < kSlices) {
+        read_b(cur, s + 1, nb);
+        read_a(cur, s + 1, na);
+      } else {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        read_b(nxt, 0, nb);
+        read_a(nxt, 0, na);
+        if (whole)
+          fetch_whole(cur);
+        else if (step + 2 < steps)
+          fetch(cur);
+      }
+#pragma unroll
+      for (int i = 0; i < C::kFM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::kFN; ++j) multiply<DT>(fb[j], fa[i], acc[i][j]);
+      // each matrix instruction followed by a share of the rest, which runs beside it
+#pragma unroll
+      for (int u = 0; u < C::kFM * C::kFN; ++u) {
+        __builtin_amdgcn_sched_group_barrier(0x008, DT == kF32 ? 4 : 1, 0);   // matrix
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                    // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                    // vector
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);                    // loads
+      }
+#pragma unroll
+      for (int i = 0; i < C::kFM; ++i) fa[i] = na[i];
+#pragma unroll
+      for (int j = 0; j < C::kFN; ++j) fb[j] = nb[j];
+    }
+    char* t = cur;
+    cur = nxt;
+    nxt = t;
+    ++step;
+  };
+  while (step < steps) {
+    for (int n = min(left / C::kBK, steps - 2 - step); n > 0; --n) multiply_step(std::true_type());
+    multiply_step(std::false_type());
+  }
+  finish<DT, BACK, C, ACT>(g, acc, m0, n0, wm, wn);
+}
+
+// Whether an operand's rows are whole 16-byte pieces whose offsets in a tile fit 32 bits.
+bool whole_pieces(const Mat& m, int width, int size) {
+  return (reinterpret_cast<uintptr_t>(m.p) | (uintptr_t)(m.ld * size) | (uintptr_t)(width * size)) %
+                 kChunk == 0 && m.ld < (1 << 20);
 }
 
 template <int DT, bool BACK, int ACT>
 hipError_t product(const Product& g, hipStream_t st) {
+  constexpr int kSize = sizeof(typename Elt<DT>::T);
+  const int width_b = BACK ? g.n : g.depth;
+  if (whole_pieces(g.a[0], g.depth, kSize) && (!BACK || whole_pieces(g.a[1], g.depth, kSize)) &&
+      whole_pieces(g.b[0], width_b, kSize) && whole_pieces(g.b[1], width_b, kSize)) {
+    typedef DirectTile<DT, BACK, 256, 256, 2, 4> C;
+    const int64_t tiles = (g.rows + C::kBM - 1) / C::kBM * ((g.n + C::kCols - 1) / C::kCols);
+    k_product_direct<DT, BACK, C, ACT><<<(unsigned)tiles, C::kThreads, 0, st>>>(g);
+    return hipGetLastError();
+  }
   typedef Tile<DT, BACK, 128, 128, 2, 2> C;
   const int64_t tiles = (g.rows + C::kBM - 1) / C::kBM * ((g.n + C::kCols - 1) / C::kCols);
   k_product<DT, BACK, C, ACT><<<(unsigned)tiles, C::kThreads, 0, st>>>(g);
