@@ -26,26 +26,77 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
 // ------------------------------------------------------------------ the activations
-// act(g) and its derivative.  p is the factor that both start from (the logistic or the normal
-// distribution function) and q what is left to 1, each formed without cancellation.
+// exp(-(x + low)) for 0 <= x <= 200 and a small correction, within 3 * 2^-24 of it: 2^t of the rounded
+// product with 1 / ln 2, and what the rounding left in first order.  (Below 2^-64 the power is taken 2^64
+// higher, as the instruction returns no denormals.)
+__device__ __forceinline__ float exp_neg(float x, float low = 0.0f) {
+  constexpr float kInv = 1.44269502f, kInvLow = 1.92596303e-8f, kLn2 = 0.69314718f;
+  const float t = -x * kInv, rest = fmaf(-low, kInv, fmaf(-x, kInvLow, fmaf(-x, kInv, -t)));
+  const bool small = t < -64.0f;
+  const float e = __builtin_amdgcn_exp2f(small ? t + 64.0f : t);
+  return fmaf(e * kLn2, rest, e) * (small ? 0x1p-64f : 1.0f);
+}
+
+// act(g) and its derivative, each within 16 * 2^-24 of its terms.  p is the factor that both start from
+// (the logistic or the normal distribution function) and q what is left to 1, each formed without
+// cancellation.  Arguments are limited to where p is 0 or 1 in fp32 anyway; NaN comes back through g.
+// These take about 25 instructions where the library's exponential, error function and division took 65
+// and more, which were 14 us of each 256 x 256 tile's time.
 template <int ACT>
 __device__ __forceinline__ void activate(float g, float* act, float* slope) {
   if (ACT == kGelu) {
-    const float p = 0.5f * erfcf(g * -0.70710678f);
+    // Phi(-a) = exp(-a^2 / 2) R(a); R, a ninth-degree polynomial in 1 / (1 + a / 4) fitted over 0 <= a
+    // <= 15 to 7e-8 of its value
+    const float a = fminf(fabsf(g), 20.0f), half = 0.5f * a, x = half * a;
+    const float e = exp_neg(x, fmaf(half, a, -x)), t = __builtin_amdgcn_rcpf(fmaf(0.25f, a, 1.0f));
+    float r = 0.024650581181049347f;
+    r = fmaf(r, t, -0.14754432439804077f);
+    r = fmaf(r, t, 0.28512391448020935f);
+    r = fmaf(r, t, -0.19303946197032928f);
+    r = fmaf(r, t, 0.19281961023807526f);
+    r = fmaf(r, t, 0.03680535778403282f);
+    r = fmaf(r, t, 0.10273300111293793f);
+    r = fmaf(r, t, 0.0986626073718071f);
+    r = fmaf(r, t, 0.09978866577148438f);
+    const float q = r * t * e, p = g >= 0.0f ? 1.0f - q : q;
     *act = g * p;
-    *slope = fmaf(g * 0.39894228f, expf(-0.5f * g * g), p);
+    *slope = fmaf(g, e * 0.39894228f, p);
     return;
   }
   constexpr float k = 1.59576912f;   // 2 sqrt(2 / pi)
-  const float v = ACT == kSilu ? g : k * fmaf(0.044715f * g * g, g, g);
-  const float e = expf(-fabsf(v)), r = 1.0f / (1.0f + e), s = e * r;
+  const float c = fminf(fmaxf(g, -30.0f), 30.0f), cubic = fmaf(0.044715f * c * c, c, c);
+  const float v = ACT == kSilu ? g : k * cubic;
+  const float e = exp_neg(fminf(fabsf(v), 200.0f));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), s = e * r;
   const float p = v >= 0.0f ? r : s, q = v >= 0.0f ? s : r;
   *act = g * p;
-  const float t = g * p * q;
-  if (ACT == kSilu)
-    *slope = p + t;
-  else   // beyond the numbers that g's square holds, t is 0
-    *slope = t == 0.0f ? p : fmaf(t, k * fmaf(0.134145f * g, g, 1.0f), p);
+  *slope = fmaf(g * p * q, ACT == kSilu ? 1.0f : k * fmaf(0.134145f * c, c, 1.0f), p);
+}
+
+// v[r] = act(v[r]) * u[r].  The forward pass stands still for this, so that silu takes a short way where
+// no lane of the wave has |g| > 16: there exp(-g) needs no correction (its argument's rounding is at most
+// 16 * 2^-24 of it) and stays far from the ends of fp32's range.
+template <int ACT, int N>
+__device__ __forceinline__ void gate(float (&v)[N], const float (&u)[N]) {
+  if (ACT == kSilu) {
+    float most = 0.0f;
+#pragma unroll
+    for (int r = 0; r < N; ++r) most = fmaxf(most, fabsf(v[r]));   // of numbers: NaN stays NaN below
+    if (__ballot(most > 16.0f) == 0) {
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float e = __builtin_amdgcn_exp2f(v[r] * -1.44269502f);
+        v[r] = v[r] * __builtin_amdgcn_rcpf(1.0f + e) * u[r];
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    float act, slope;
+    activate<ACT>(v[r], &act, &slope);
+    v[r] = act * u[r];
+  }
 }
 
 template <int DT, int ACT>
@@ -80,6 +131,8 @@ struct Product {
                          // the two weights (depth x n)
   Mat out[3];            // forward: h, gate, up (the last two may be null); backward: dx
   int32_t act;
+  int32_t splits;        // parts of the sum; with more than one, part i of result j (forward: gate, up;
+  float* ws;             // backward: dx) goes to ws[i][j][rows][n]
 };
 
 constexpr int kChunk = 16, kRowBytes = 128, kRowChunks = kRowBytes / kChunk;
@@ -94,12 +147,14 @@ struct Tile {
   static constexpr int kFM = BM / WM / 32, kFN = BN / WN / 32;
   static constexpr int kElts = kChunk / (int)sizeof(T), kBK = kRowChunks * kElts;
   static constexpr int kCols = BACK ? BN : BN / 2;      // of the result
-  // backward: 64 bytes past a row, so that the four rows of a transposing read start in different
-  // quarters of the banks
-  static constexpr int kPitchB = BACK ? BN * (int)sizeof(T) + 64 : kRowBytes;
+  static constexpr int kPiecesB = BACK ? BN / kElts : kRowChunks;   // of a row of the second operand
+  static constexpr int kPitchB = kPiecesB * kChunk;
   static constexpr int kBytesA = BM * kRowBytes, kBytesB = (BACK ? kBK : BN) * kPitchB;
-  static constexpr int kItemsA = BM * kRowChunks / kThreads;
-  static constexpr int kItemsB = BACK ? kBK * (BN / kElts) / kThreads : BN * kRowChunks / kThreads;
+  static constexpr int kStage = kBytesA + kBytesB;
+  // Loading: an item is one piece a thread, kRowsA rows of a step's first or kRowsB of its second operand.
+  static constexpr int kRowsA = kThreads / kRowChunks, kRowsB = kThreads / kPiecesB;
+  static constexpr int kItemsA = kBytesA / kChunk / kThreads, kItemsB = kBytesB / kChunk / kThreads;
+  static_assert(BN >= 128 && (BACK || (kFN % 2 == 0 && kRowsB % 16 == 0 && kRowsB <= 64)), "layouts");
 };
 
 // Where 16-byte piece c of row r of a tile lies: the pieces of 16 neighbouring rows that a read takes
@@ -108,24 +163,42 @@ __device__ __forceinline__ int piece_at(int r, int c) {
   return r * kRowBytes + ((c ^ ((r >> 1) & (kRowChunks - 1))) * kChunk);
 }
 
+// Where the 64-byte block b of row r lies in a row of the backward pass's second operand: the four rows
+// of a transposing read (fp32: the two halves of a wave, four rows apart) in different banks.
+template <int DT>
+__device__ __forceinline__ int block_at(int r, int b) {
+  return DT == kF32 ? b ^ ((r >> 1) & 2) : b ^ (r & 3);
+}
+
 // The column (of 32) that row i of a product's first operand stands for: a lane's 16 registers hold
 // rows 8 * (r / 4) + 4 * (lane / 32) + r % 4, and are to be columns 16 * (lane / 32) + r.
 __device__ __forceinline__ int column_of(int i) {
   return 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);
 }
 
-// 16 bytes of the row at p from element k on, zeros from `end` on.
+// 16 bytes of the row at p from element k on, zeros from `end` on.  Where the row ends inside them its last
+// 16 bytes are loaded and moved into place.
 template <typename T>
 __device__ __forceinline__ u4 load_piece(const T* p, int k, int end) {
   constexpr int E = 16 / sizeof(T);
-  if (k + E <= end) return *reinterpret_cast<const u4_at_any*>(p + k);
-  T v[E] = {};
+  uint32_t d[4] = {};
+  if (end >= E) {
+    const int at = min(k, end - E), over = min(k - at, E - 1);
+    __builtin_memcpy(d, p + at, sizeof d);
+    shift_down<4>(d, (uint32_t)over * (sizeof(T) / 2));
+  } else {   // a row of less than 16 bytes: from its end, each element under the last
+#pragma unroll 1
+    for (int j = end - 1; j >= k; --j) {
+      uint32_t e = 0;
+      __builtin_memcpy(&e, p + j, sizeof(T));
 #pragma unroll
-  for (int j = 0; j < E; ++j)
-    if (k + j < end) v[j] = p[k + j];
-  u4 w;
-  __builtin_memcpy(&w, v, sizeof w);
-  return w;
+      for (int i = 3; i >= 0; --i) {
+        const uint32_t below = i ? d[i - 1] : (sizeof(T) == 2 ? e << 16 : e);
+        d[i] = sizeof(T) == 2 ? (d[i] << 16) | (below >> 16) : below;
+      }
+    }
+  }
+  return k < end ? u4{d[0], d[1], d[2], d[3]} : u4{};
 }
 
 // acc += a b for 16 bytes of the summed dimension a lane.
@@ -145,266 +218,190 @@ __device__ __forceinline__ void multiply(const u4& w, const u4& x, f16v& acc) {
   }
 }
 
-// Rounds and stores a wave's products, of the forward pass after the activation.
-template <int DT, bool BACK, typename C, int ACT>
-__device__ __forceinline__ void finish(const Product& g, const f16v (&acc)[C::kFM][C::kFN],
+// Stores a block of 32 rows x 32 B columns, of which a lane holds 16 columns of one row (a row of 16 halves
+// on two lanes, 32 apart).  Lanes that follow each other in memory are 32 apart in the wave, so that
+// stores as they lie took four 16-byte requests for 64 bytes; the block goes through the wave's own part
+// of LDS instead, and comes back with 4 and more neighbouring lanes a row.  INSIDE: all columns exist.
+template <typename T, int B, bool INSIDE>
+__device__ __forceinline__ void store_block(char* lds, T* p, int64_t ld, int64_t row0, int64_t rows,
+                                            int col0, int n, const float (&v)[B][16]) {
+  constexpr int E = kChunk / sizeof(T), P = 32 * B / E;   // pieces of a row
+  static_assert(P <= 16, "a row within the banks");
+  const int half = lane_id() >> 5, in = lane_id() & 31;
+  // piece c of row r: pieces of neighbouring rows in different banks
+  auto at = [&](int r, int c) { return (r * P + (c ^ ((r / (16 / P)) & (P - 1)))) * kChunk; };
+  constexpr int DT = sizeof(T) == 4 ? kF32 : std::is_same<T, __bf16>::value ? kBF16 : kF16;
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+#pragma unroll
+    for (int q = 0; q < 16 / E; ++q) {
+      T t[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) t[e] = round_to<DT>(v[b][q * E + e]);
+      u4 w;
+      __builtin_memcpy(&w, t, sizeof w);
+      *reinterpret_cast<u4*>(lds + at(in, (32 * b + 16 * half) / E + q)) = w;
+    }
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    const int k = i * 64 + lane_id(), r = k / P, c = k % P, col = col0 + c * E;
+    const u4 w = *reinterpret_cast<const u4*>(lds + at(r, c));
+    if (row0 + r >= rows) continue;
+    T* q = p + (row0 + r) * ld + col;
+    if (INSIDE || col + E <= n) {
+      *reinterpret_cast<u4_at_any*>(q) = w;
+    } else {
+      T t[E];
+      __builtin_memcpy(t, &w, sizeof w);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (col + e < n) q[e] = t[e];
+    }
+  }
+}
+
+// Stores a wave's products: the results, of the forward pass after the activation, or a part of the sums.
+template <int DT, bool BACK, typename C, int ACT, bool INSIDE>
+__device__ __forceinline__ void finish(const Product& g, const f16v (&acc)[C::kFM][C::kFN], char* lds,
                                        int64_t m0, int n0, int wm, int wn) {
   typedef typename Elt<DT>::T T;
-  const int half = lane_id() >> 5, in = lane_id() & 31;
+  constexpr int B = BACK ? C::kFN : C::kFN / 2;
+  const int col = n0 + (BACK ? wn : wn / 2);
 #pragma unroll
   for (int i = 0; i < C::kFM; ++i) {
-    const int64_t row = m0 + wm + 32 * i + in;
-    if (row >= g.rows) continue;
-    auto put = [&](const Mat& m, int col, const float (&v)[8]) {
-      store8<DT>(static_cast<T*>(m.p) + row * m.ld, col, g.n, v);
+    const int64_t row = m0 + wm + 32 * i;
+    auto put = [&](const Mat& m, const float (&v)[B][16]) {
+      store_block<T, B, INSIDE>(lds, static_cast<T*>(m.p), m.ld, row, g.rows, col, g.n, v);
     };
+    float v[B][16], u[B][16];
 #pragma unroll
-    for (int j = 0; j < C::kFN; j += BACK ? 1 : 2)
+    for (int b = 0; b < B; ++b)
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int col = n0 + (BACK ? wn + 32 * j : wn / 2 + 16 * j) + 16 * half + 8 * o;
-        if (col >= g.n) continue;
-        float v[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = acc[i][j][8 * o + r];
-        if constexpr (BACK) {
-          put(g.out[0], col, v);
-        } else {
-          float u[8];
-#pragma unroll
-          for (int r = 0; r < 8; ++r) u[r] = acc[i][j + 1][8 * o + r];
-          if (g.out[1].p) put(g.out[1], col, v);
-          if (g.out[2].p) put(g.out[2], col, u);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            float act, slope;
-            activate<ACT>(v[r], &act, &slope);
-            v[r] = act * u[r];
-          }
-          put(g.out[0], col, v);
-        }
+      for (int r = 0; r < 16; ++r) {
+        v[b][r] = acc[i][BACK ? b : 2 * b][r];
+        u[b][r] = acc[i][BACK ? b : 2 * b + 1][r];
       }
-  }
-}
-
-template <int DT, bool BACK, typename C, int ACT>
-__global__ __launch_bounds__(C::kThreads) void k_product(Product g) {
-  typedef typename Elt<DT>::T T;
-  constexpr int E = C::kElts;
-  __shared__ __align__(16) char s_mem[2 * (C::kBytesA + C::kBytesB)];
-  const int tiles_m = (int)((g.rows + C::kBM - 1) / C::kBM);
-  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * C::kBM;
-  const int n0 = (int)(blockIdx.x / tiles_m) * C::kCols;
-  const int lane = lane_id(), wave = wave_id();
-  const int wm = wave / C::kWN * (C::kFM * 32), wn = wave % C::kWN * (C::kFN * 32);
-  const int steps_seg = (g.depth + C::kBK - 1) / C::kBK, steps = BACK ? 2 * steps_seg : steps_seg;
-
-  u4 ra[C::kItemsA], rb[C::kItemsB];
-  auto load = [&](int step) {
-    const int seg = BACK && step >= steps_seg, k0 = (step - seg * steps_seg) * C::kBK;
-#pragma unroll
-    for (int p = 0; p < C::kItemsA; ++p) {
-      const int at = p * C::kThreads + threadIdx.x, r = at / kRowChunks, c = at % kRowChunks;
-      const int64_t row = min(m0 + r, g.rows - 1);
-      ra[p] = load_piece(static_cast<const T*>(g.a[seg].p) + row * g.a[seg].ld, k0 + c * E, g.depth);
-    }
-#pragma unroll
-    for (int p = 0; p < C::kItemsB; ++p) {
-      const int at = p * C::kThreads + threadIdx.x;
-      if (BACK) {
-        const int r = k0 + at / (C::kBN / E), c = at % (C::kBN / E);
-        rb[p] = r < g.depth ? load_piece(static_cast<const T*>(g.b[seg].p) + (int64_t)r * g.b[seg].ld,
-                                         n0 + c * E, g.n)
-                            : u4{};
-      } else {
-        const int r = at / kRowChunks, c = at % kRowChunks, w = (r >> 5) & 1;
-        const int row = min(n0 + (r >> 6) * 32 + column_of(r & 31), g.n - 1);
-        rb[p] = load_piece(static_cast<const T*>(g.b[w].p) + (int64_t)row * g.b[w].ld, k0 + c * E,
-                           g.depth);
-      }
-    }
-  };
-  auto store = [&](char* stage) {
-#pragma unroll
-    for (int p = 0; p < C::kItemsA; ++p) {
-      const int at = p * C::kThreads + threadIdx.x;
-      *reinterpret_cast<u4*>(stage + piece_at(at / kRowChunks, at % kRowChunks)) = ra[p];
-    }
-#pragma unroll
-    for (int p = 0; p < C::kItemsB; ++p) {
-      const int at = p * C::kThreads + threadIdx.x;
-      char* q = stage + C::kBytesA;
-      if (BACK)
-        q += at / (C::kBN / E) * C::kPitchB + at % (C::kBN / E) * kChunk;
-      else
-        q += piece_at(at / kRowChunks, at % kRowChunks);
-      *reinterpret_cast<u4*>(q) = rb[p];
-    }
-  };
-  const int half = lane >> 5, in = lane & 31;
-  auto read_a = [&](const char* stage, int s, int i) {
-    return *reinterpret_cast<const u4*>(stage + piece_at(wm + 32 * i + in, 2 * s + half));
-  };
-  auto read_b = [&](const char* stage, int s, int j) {
-    const char* q = stage + C::kBytesA;
-    if constexpr (!BACK) {
-      return *reinterpret_cast<const u4*>(q + piece_at(wn + 32 * j + in, 2 * s + half));
-    } else if constexpr (DT == kF32) {
-      q += (2 * s + half) * E * C::kPitchB + (wn + 32 * j + column_of(in)) * 4;
-      u4 w;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint32_t*>(q + t * C::kPitchB);
-      return w;
+    if (g.splits > 1) {
+      float* part = g.ws + (int64_t)blockIdx.y * (BACK ? 1 : 2) * g.rows * g.n;
+      store_block<float, B, INSIDE>(lds, part, g.n, row, g.rows, col, g.n, v);
+      if (!BACK) store_block<float, B, INSIDE>(lds, part + g.rows * g.n, g.n, row, g.rows, col, g.n, u);
+    } else if (BACK) {
+      put(g.out[0], v);
     } else {
-      // four rows of 16 columns for 16 lanes; the lanes' groups of 4 columns in the products' order
-      const int group = 4 * ((lane >> 4) & 1) + (lane & 3);
-      q += ((2 * s + half) * E + ((lane & 15) >> 2)) * C::kPitchB +
-           (wn + 32 * j + 16 * (group & 1) + 4 * (group >> 1)) * 2;
-      const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)q);
-      const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + 4 * C::kPitchB));
-      return __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      if (g.out[1].p) put(g.out[1], v);
+      if (g.out[2].p) put(g.out[2], u);
+#pragma unroll
+      for (int b = 0; b < B; ++b) gate<ACT, 16>(v[b], u[b]);
+      put(g.out[0], v);
     }
-  };
-
-  f16v acc[C::kFM][C::kFN] = {};
-  char *cur = s_mem, *nxt = s_mem + C::kBytesA + C::kBytesB;
-  if (steps) {
-    load(0);
-    store(cur);
   }
-  __syncthreads();
-  for (int step = 0; step < steps; ++step) {
-    if (step + 1 < steps) load(step + 1);
-#pragma unroll
-    for (int s = 0; s < kRowChunks / 2; ++s) {
-      u4 fa[C::kFM], fb[C::kFN];
-#pragma unroll
-      for (int i = 0; i < C::kFM; ++i) fa[i] = read_a(cur, s, i);
-#pragma unroll
-      for (int j = 0; j < C::kFN; ++j) fb[j] = read_b(cur, s, j);
-#pragma unroll
-      for (int i = 0; i < C::kFM; ++i)
-#pragma unroll
-        for (int j = 0; j < C::kFN; ++j) multiply<DT>(fb[j], fa[i], acc[i][j]);
-    }
-    if (step + 1 < steps) store(nxt);
-    __syncthreads();
-    char* t = cur;
-    cur = nxt;
-    nxt = t;
-  }
-
-  finish<DT, BACK, C, ACT>(g, acc, m0, n0, wm, wn);
 }
 
-// ------------------------------------------------------------------ whole pieces: loaded into LDS directly
-// The same product where every row of an operand starts on 16 bytes and holds whole 16-byte pieces:
-// the loads write LDS themselves, a wave 1024 bytes of a stage at a time, in the order of the lanes; so
-// what a lane loads is what belongs into its place, and the places of a row's pieces are permuted as
-// above without a gap between rows.
-__device__ const u4 g_zeros = {0, 0, 0, 0};
-
-typedef __attribute__((address_space(1))) const void global_void;
-typedef __attribute__((address_space(3))) void lds_void;
-
-template <int DT, bool BACK, int BM, int BN, int WM, int WN>
-struct DirectTile : Tile<DT, BACK, BM, BN, WM, WN> {
-  typedef Tile<DT, BACK, BM, BN, WM, WN> Base;
-  // pieces of a row of the second operand's stage
-  static constexpr int kPiecesB = BACK ? BN / Base::kElts : kRowChunks;
-  static constexpr int kPitchB = kPiecesB * kChunk;
-  static constexpr int kBytesB = (BACK ? Base::kBK : BN) * kPitchB, kStage = Base::kBytesA + kBytesB;
-  static constexpr int kRowsA = Base::kThreads / kRowChunks, kRowsB = Base::kThreads / kPiecesB;
-};
-
-// Where the 64-byte block b of row r lies in a row of the second operand (backward): the four rows of a
-// transposing read (fp32: the two halves of a wave, four rows apart) in different banks.
-template <int DT>
-__device__ __forceinline__ int block_at(int r, int b) {
-  return DT == kF32 ? b ^ ((r >> 1) & 2) : b ^ (r & 3);
+// Tile of this workgroup.  Workgroups go to the 8 XCDs in turn: each XCD gets a contiguous range of the
+// order below, in which kBand tiles of rows share their part of the second operand, and its L2 holds what
+// they share.
+constexpr int kBand = 4;
+__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int* tm, int* tn) {
+  const int total = tiles_m * tiles_n, id = blockIdx.x;
+  const int q = total / 8, r = total % 8, xcd = id % 8, i = id / 8;
+  const int t = xcd < r ? xcd * (q + 1) + i : r * (q + 1) + (xcd - r) * q + i;
+  const int band = t / (kBand * tiles_n), high = min(kBand, tiles_m - kBand * band);
+  const int in = t - band * kBand * tiles_n;
+  *tm = kBand * band + in % high;
+  *tn = in / high;
 }
 
 template <int DT, bool BACK, typename C, int ACT>
-__global__ __launch_bounds__(C::kThreads, 2) void k_product_direct(Product g) {
+__global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
   typedef typename Elt<DT>::T T;
-  constexpr int E = C::kElts;
+  constexpr int E = C::kElts, kItems = C::kItemsA + C::kItemsB, kSlices = kRowChunks / 2;
+  constexpr int64_t kSize = sizeof(T);
   __shared__ __align__(16) char s_mem[2 * C::kStage];
-  const int tiles_m = (int)((g.rows + C::kBM - 1) / C::kBM);
-  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * C::kBM;
-  const int n0 = (int)(blockIdx.x / tiles_m) * C::kCols;
+  int tm, tn;
+  tile_of((int)((g.rows + C::kBM - 1) / C::kBM), (g.n + C::kCols - 1) / C::kCols, &tm, &tn);
+  const int64_t m0 = (int64_t)tm * C::kBM;
+  const int n0 = tn * C::kCols;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int wm = wave / C::kWN * (C::kFM * 32), wn = wave % C::kWN * (C::kFN * 32);
-  const int steps_seg = (g.depth + C::kBK - 1) / C::kBK, steps = BACK ? 2 * steps_seg : steps_seg;
+  const int steps_seg = (g.depth + C::kBK - 1) / C::kBK, all_steps = (BACK ? 2 : 1) * steps_seg;
+  const int first = (int)((int64_t)all_steps * blockIdx.y / g.splits);
+  const int steps = (int)((int64_t)all_steps * (blockIdx.y + 1) / g.splits) - first;
 
   // This thread's piece of every item: A's row p * kRowsA + ra, piece ca of the step; B's likewise.
   const int ra = threadIdx.x / kRowChunks, ca = (threadIdx.x % kRowChunks) ^ ((ra >> 1) & 7);
   const int rb = threadIdx.x / C::kPiecesB, sb = threadIdx.x % C::kPiecesB;
   const int cb = BACK ? block_at<DT>(rb, sb >> 2) * 4 + (sb & 3) : sb ^ ((rb >> 1) & 7);
-  // The place of the next step to be fetched, the same in all lanes, and from it the byte offset of each
-  // item's row (rows past the last one read it, columns past the last one the tile's first; what they
-  // add up is not stored).
+  // Where the rows of the items lie from the tile's first (rows past the last one read it; what they add
+  // up is not stored).
+  auto row_a = [&](int p) { return min(m0 + p * C::kRowsA + ra, g.rows - 1) - m0; };
+  auto row_b = [&](int p) {
+    const int r = p * C::kRowsB + rb;
+    return (int64_t)(BACK ? r : min(n0 + (r >> 6) * 32 + column_of(r & 31), g.n - 1) - n0);
+  };
+  int seg = 0, left = 0;   // of the sum, from the next step on: the segment, what is left of it
+  // Forward: a wave loads 8 rows at a time, of one of the weights: always the same, or by the item.
+  auto weight = [&](int p) {
+    return BACK ? seg : C::kRowsB == 64 ? (wave >> 2) & 1 : (p * C::kRowsB >> 5) & 1;
+  };
+  // The place of the next step to be loaded, the same in all lanes, and from it the byte offset of each
+  // item's piece (columns past the last one are the tile's first).
   const char *pa, *pb[2];
   int64_t next_b;
   uint32_t off_a[C::kItemsA], off_b[C::kItemsB];
-  int left;              // of the segment's sum, from the next step on
-  auto start = [&](int seg) {
+  auto start = [&](int which, int from) {
+    seg = which;
     const Mat& a = g.a[seg];
-    left = g.depth;
-    pa = static_cast<const char*>(a.p) + m0 * a.ld * (int64_t)sizeof(T);
-    if (BACK) {
-      pb[0] = static_cast<const char*>(g.b[seg].p) + n0 * (int64_t)sizeof(T);
-      next_b = C::kBK * g.b[seg].ld * (int64_t)sizeof(T);
-    } else {
-      // a wave loads 8 rows at a time, of one of the weights: always the same or each in turn
-      const int w = C::kRowsB == 64 ? (wave >> 2) & 1 : 0;
-      pb[0] = static_cast<const char*>(g.b[w].p) + n0 * g.b[w].ld * (int64_t)sizeof(T);
-      pb[1] = static_cast<const char*>(g.b[1].p) + n0 * g.b[1].ld * (int64_t)sizeof(T);
-      next_b = kRowBytes;
+    left = g.depth - from * C::kBK;
+    pa = static_cast<const char*>(a.p) + m0 * a.ld * kSize + (int64_t)from * kRowBytes;
+    next_b = BACK ? C::kBK * g.b[seg].ld * kSize : kRowBytes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Mat& b = g.b[BACK ? seg : C::kRowsB == 64 ? (wave >> 2) & 1 : i];
+      pb[i] = static_cast<const char*>(b.p) + (BACK ? (int64_t)n0 : n0 * b.ld) * kSize + from * next_b;
     }
 #pragma unroll
-    for (int p = 0; p < C::kItemsA; ++p)
-      off_a[p] = (uint32_t)((min(m0 + p * C::kRowsA + ra, g.rows - 1) - m0) * a.ld *
-                            (int64_t)sizeof(T)) + ca * kChunk;
+    for (int p = 0; p < C::kItemsA; ++p) off_a[p] = (uint32_t)(row_a(p) * a.ld * kSize) + ca * kChunk;
 #pragma unroll
-    for (int p = 0; p < C::kItemsB; ++p) {
-      const int r = p * C::kRowsB + rb;
-      const int64_t pitch = g.b[BACK ? seg : (r >> 5) & 1].ld * (int64_t)sizeof(T);
-      if (BACK)
-        off_b[p] = (uint32_t)(r * pitch) + (n0 + cb * E < g.n ? cb * kChunk : 0);
-      else
-        off_b[p] = (uint32_t)((min(n0 + (r >> 6) * 32 + column_of(r & 31), g.n - 1) - n0) * pitch) +
-                   cb * kChunk;
-    }
+    for (int p = 0; p < C::kItemsB; ++p)
+      off_b[p] = (uint32_t)(row_b(p) * g.b[weight(p)].ld * kSize) +
+                 (BACK && n0 + cb * E >= g.n ? 0 : cb * kChunk);
   };
-  auto item = [&](char* stage, const char* src, int p) {
-    __builtin_amdgcn_global_load_lds(
-        (global_void*)src, (lds_void*)(stage + wave * (64 * kChunk) + p * C::kThreads * kChunk),
-        kChunk, 0, 0);
-  };
-  auto from_b = [&](int p) { return pb[BACK || C::kRowsB == 64 ? 0 : p & 1] + off_b[p]; };
+  auto base_b = [&](int p) { return pb[BACK || C::kRowsB == 64 ? 0 : (p * C::kRowsB >> 5) & 1]; };
   auto advance = [&] {
     pa += kRowBytes;
     pb[0] += next_b;
-    if (!BACK) pb[1] += next_b;
+    pb[1] += next_b;
     left -= C::kBK;
   };
-  // The next step into a stage: one that is whole, and any; pieces behind the sum's end come from zeros.
-  auto fetch_whole = [&](char* stage) {
-#pragma unroll
-    for (int p = 0; p < C::kItemsA; ++p) item(stage, pa + off_a[p], p);
-#pragma unroll
-    for (int p = 0; p < C::kItemsB; ++p) item(stage, from_b(p), C::kItemsA + p);
-    advance();
+  u4 reg[kItems];
+  // Item p of the next step, A's first: of a step that is whole (all of its pieces are there), and of
+  // any: what lies behind the sum's end is 0.
+  auto load_whole = [&](int p) {
+    const char* q = p < C::kItemsA ? pa + off_a[p] : base_b(p - C::kItemsA) + off_b[p - C::kItemsA];
+    reg[p] = *reinterpret_cast<const u4_at_any*>(q);
   };
-  auto fetch = [&](char* stage) {
-    if (BACK && left <= 0) start(1);
-    const char* none = reinterpret_cast<const char*>(&g_zeros);
-#pragma unroll
-    for (int p = 0; p < C::kItemsA; ++p) item(stage, ca * E < left ? pa + off_a[p] : none, p);
-#pragma unroll
-    for (int p = 0; p < C::kItemsB; ++p)
-      item(stage, (BACK ? p * C::kRowsB + rb : cb * E) < left ? from_b(p) : none, C::kItemsA + p);
-    advance();
+  auto load_edge = [&](int p) {
+    if (p < C::kItemsA) {
+      const char* q = pa + row_a(p) * g.a[seg].ld * kSize;
+      reg[p] = load_piece(reinterpret_cast<const T*>(q), ca * E, left);
+    } else {
+      const int b = p - C::kItemsA;
+      const int64_t row = BACK ? min(row_b(b), (int64_t)left - 1) : row_b(b);
+      const char* q = base_b(b) + row * g.b[weight(b)].ld * kSize;
+      reg[p] = load_piece(reinterpret_cast<const T*>(q), cb * E, BACK ? g.n - n0 : left);
+      if (BACK && row_b(b) >= left) reg[p] = u4{};
+    }
+  };
+  auto store = [&](char* stage, int p) {
+    *reinterpret_cast<u4*>(stage + (p * C::kThreads + threadIdx.x) * kChunk) = reg[p];
+  };
+  // Steps that can be loaded whole from here on: none where the offsets in a tile pass 32 bits.  (A piece
+  // that starts inside a row of the backward pass's weight but ends behind it reads on into the next row,
+  // which the last one has not.)
+  auto whole_steps = [&] {
+    const int64_t widest = max(g.a[seg].ld, max(g.b[BACK ? seg : 0].ld, g.b[BACK ? seg : 1].ld));
+    if (widest >= (1 << 21) || (BACK && g.b[seg].ld < E)) return 0;
+    return (BACK && n0 + C::kBN > g.n ? left - 1 : left) / C::kBK;
   };
 
   const int half = lane >> 5, in = lane & 31;
@@ -426,6 +423,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product_direct(Product g) {
         for (int e = 0; e < 4; ++e)
           f[j][e] = *reinterpret_cast<const uint32_t*>(t + e * C::kPitchB);
       } else {
+        // four rows of 16 columns for 16 lanes; the lanes' groups of 4 columns in the products' order
         const int group = 4 * ((lane >> 4) & 1) + (lane & 3), r4 = (lane & 15) >> 2;
         const char* t = q + ((2 * s + half) * E + r4) * C::kPitchB +
                         block_at<DT>(r4, (wn + 32 * j) >> 5) * 64 +
@@ -437,45 +435,64 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product_direct(Product g) {
     }
   };
 
-  constexpr int kItems = C::kItemsA + C::kItemsB, kSlices = kRowChunks / 2;
-  static_assert(BACK || C::kRowsB == 64 || C::kRowsB == 32, "an item's rows of a wave are of one weight");
+  // The next step, whichever it is.
+  auto load_step = [&] {
+    if (BACK && left <= 0 && seg == 0) start(1, 0);
+#pragma unroll
+    for (int p = 0; p < kItems; ++p) {
+      load_edge(p);
+      __builtin_amdgcn_sched_barrier(0);   // one after the other: few registers
+    }
+    advance();
+  };
+
   f16v acc[C::kFM][C::kFN] = {};
   char *cur = s_mem, *nxt = s_mem + C::kStage;
   u4 fa[C::kFM], fb[C::kFN];
-  if (steps) {
-    start(0);
-    fetch(cur);
-    asm volatile("" ::: "memory");
-    if (steps > 1) {
-      fetch(nxt);
-      // the first stage's loads are done when at most the second's are left
-      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kItems) : "memory");
+  if (steps > 0) {
+    start(first >= steps_seg, first >= steps_seg ? first - steps_seg : first);
+    if (steps > 1 && whole_steps() > 1) {   // both steps' loads on their way at once
+      u4 ahead[kItems];
+#pragma unroll
+      for (int p = 0; p < kItems; ++p) load_whole(p);
+      advance();
+#pragma unroll
+      for (int p = 0; p < kItems; ++p) {
+        ahead[p] = reg[p];
+        load_whole(p);
+      }
+      advance();
+#pragma unroll
+      for (int p = 0; p < kItems; ++p)
+        *reinterpret_cast<u4*>(cur + (p * C::kThreads + threadIdx.x) * kChunk) = ahead[p];
     } else {
-      asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+      load_step();
+#pragma unroll
+      for (int p = 0; p < kItems; ++p) store(cur, p);
+      if (steps > 1) load_step();
     }
-    read_a(cur, 0, fa);
+    __syncthreads();
     read_b(cur, 0, fb);
+    read_a(cur, 0, fa);
   }
-  // One step: each slice is multiplied while the operands of the next are read.  Before the last one all
-  // waves meet: the next stage has arrived then and nobody reads this one any more, so that the step
-  // after the next goes there.
+  // One step: each slice is multiplied while the operands of the next are read.  During all slices but the
+  // last the next step's pieces, loaded a step ago, go to the other stage, each followed by the load of
+  // the piece of the step after, where that is whole.  Before the last slice all waves meet: the other
+  // stage is complete then, and nobody reads this one any more.
   int step = 0;
-  auto multiply_step = [&](auto whole) {
+  auto multiply_step = [&](auto load) {
 #pragma unroll
     for (int s = 0; s < kSlices; ++s) {
       u4 na[C::kFM], nb[C::kFN];
-      if (s + 1 < kSlices) {
-        read_b(cur, s + 1, nb);
-        read_a(cur, s + 1, na);
-      } else {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        read_b(nxt, 0, nb);
-        read_a(nxt, 0, na);
-        if (whole)
-          fetch_whole(cur);
-        else if (step + 2 < steps)
-          fetch(cur);
-      }
+      if (s + 1 == kSlices) __syncthreads();
+      read_b(s + 1 < kSlices ? cur : nxt, (s + 1) % kSlices, nb);
+      read_a(s + 1 < kSlices ? cur : nxt, (s + 1) % kSlices, na);
+#pragma unroll
+      for (int p = 0; p < kItems; ++p)
+        if (p * (kSlices - 1) / kItems == s) {
+          store(nxt, p);
+          if (load) load_whole(p);
+        }
 #pragma unroll
       for (int i = 0; i < C::kFM; ++i)
 #pragma unroll
@@ -486,45 +503,160 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product_direct(Product g) {
         __builtin_amdgcn_sched_group_barrier(0x008, DT == kF32 ? 4 : 1, 0);   // matrix
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                    // LDS reads
         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                    // vector
-        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);                    // loads
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                    // loads
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);                    // LDS writes
       }
 #pragma unroll
       for (int i = 0; i < C::kFM; ++i) fa[i] = na[i];
 #pragma unroll
       for (int j = 0; j < C::kFN; ++j) fb[j] = nb[j];
     }
+    if (load) advance();
     char* t = cur;
     cur = nxt;
     nxt = t;
     ++step;
   };
   while (step < steps) {
-    for (int n = min(left / C::kBK, steps - 2 - step); n > 0; --n) multiply_step(std::true_type());
+    if (BACK && left <= 0 && seg == 0) start(1, 0);
+    for (int n = min(whole_steps(), steps - 2 - step); n > 0; --n)
+      multiply_step(std::true_type());
+    if (BACK && left <= 0 && seg == 0 && step + 2 < steps) continue;
     multiply_step(std::false_type());
+    if (step + 1 < steps) load_step();   // the step after the next: step is one further now
   }
-  finish<DT, BACK, C, ACT>(g, acc, m0, n0, wm, wn);
+  // each wave's own part of LDS, which all have stopped reading
+  constexpr int kPart = 2 * C::kStage / (C::kThreads / 64);
+  static_assert(kPart >= 32 * 32 * (BACK ? C::kFN : C::kFN / 2) * 4, "a block of fp32");
+  char* lds = s_mem + wave * kPart;
+  if (n0 + C::kCols <= g.n)
+    finish<DT, BACK, C, ACT, true>(g, acc, lds, m0, n0, wm, wn);
+  else
+    finish<DT, BACK, C, ACT, false>(g, acc, lds, m0, n0, wm, wn);
 }
 
-// Whether an operand's rows are whole 16-byte pieces whose offsets in a tile fit 32 bits.
-bool whole_pieces(const Mat& m, int width, int size) {
-  return (reinterpret_cast<uintptr_t>(m.p) | (uintptr_t)(m.ld * size) | (uintptr_t)(width * size)) %
-                 kChunk == 0 && m.ld < (1 << 20);
+// The parts of the sums joined in order, 8 columns a thread.
+template <int DT, bool BACK, int ACT>
+__global__ __launch_bounds__(256) void k_product_join(Product g) {
+  typedef typename Elt<DT>::T T;
+  const int octets = (g.n + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / octets;
+  if (row >= g.rows) return;
+  const int col = (int)(i - row * octets) * 8;
+  const int64_t part = (BACK ? 1 : 2) * g.rows * g.n;
+  float v[8] = {}, u[8] = {};
+  auto add = [&](const float* p, float (&sum)[8]) {
+    for (int s = 0; s < g.splits; s += 4) {   // 4 parts in flight
+      float w[4][8] = {};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (s + t < g.splits) load8<kF32>(p + (s + t) * part, col, g.n, w[t]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += w[t][j];
+    }
+  };
+  add(g.ws + row * g.n, v);
+  if (!BACK) add(g.ws + (g.rows + row) * g.n, u);
+  auto put = [&](const Mat& m, const float (&w)[8]) {
+    store8<DT>(static_cast<T*>(m.p) + row * m.ld, col, g.n, w);
+  };
+  if (!BACK) {
+    if (g.out[1].p) put(g.out[1], v);
+    if (g.out[2].p) put(g.out[2], u);
+    gate<ACT, 8>(v, u);
+  }
+  put(g.out[0], v);
+}
+
+template <int DT, bool BACK, int ACT, typename C>
+hipError_t product(const Product& g, hipStream_t st) {
+  const int64_t tiles = (g.rows + C::kBM - 1) / C::kBM * ((g.n + C::kCols - 1) / C::kCols);
+  k_product<DT, BACK, C, ACT><<<dim3((unsigned)tiles, g.splits), C::kThreads, 0, st>>>(g);
+  return hipGetLastError();
+}
+
+template <int DT, bool BACK>
+using Large = Tile<DT, BACK, 256, 256, 2, 4>;
+template <int DT, bool BACK>
+using Small = Tile<DT, BACK, 128, 128, 2, 2>;
+template <int DT, bool BACK>
+using Tiny = Tile<DT, BACK, 64, 128, 2, 2>;
+
+enum TileKind { kLarge, kSmall, kTiny };
+
+struct Shape {
+  TileKind tile;
+  int splits;
+};
+
+// A large tile needs the fewest loads a product, but leaves CUs idle where the result is small; a long sum
+// can be split over CUs, at the price of writing and joining its parts.  The tile and the split with the
+// least estimated time are taken.  A step (64 summed columns of the 16-bit types, 32 of fp32) of a tile
+// takes, with 1, 2 and 3 workgroups on its CU, in microseconds (measured; a CU holds 1 large, 2 small or 3
+// tiny ones):
+//              large          small        tiny
+//   16 bits    1.15 or 1.72   0.53 1.0     0.50 0.69 1.05   (large: on up to half of the CUs, or all)
+//   fp32       -              1.95 3.84    1.1  2.1  3.2
+// and a round of tiles 14, 7 or 4 us besides (launch, first loads, the results' way); a join 4 us, 0.25 us a
+// part and their bytes (written and read) at 5 TB/s.  In fp32 a large tile gains 5 % over small ones.  Where the
+// rows' widths are not whole 16 bytes, as where they start anywhere, a large step takes 1.15 times and the
+// others 1.45 times as long.
+Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
+  constexpr int kRows[3] = {256, 128, 64}, kColumns[3] = {256, 128, 128}, kPerCU[3] = {1, 2, 3};
+  constexpr double kRound[3] = {14.0, 7.0, 4.0};
+  constexpr double kStep16[3][3] = {{1.72}, {0.53, 1.0}, {0.50, 0.69, 1.05}};
+  constexpr double kStep32[3][3] = {{}, {1.95, 3.84}, {1.1, 2.1, 3.2}};
+  constexpr int64_t kCUs = 256;
+  const int bk = dtype == kF32 ? 32 : 64;
+  const int64_t steps = (back ? 2 : 1) * (((int64_t)depth + bk - 1) / bk);
+  const bool ragged = depth % (bk / 8) || (back && n % (bk / 8));
+  Shape best = {kTiny, 1};
+  double least = 1e300;
+  for (int t = dtype == kF32 ? 1 : 0; t < 3; ++t) {
+    const int columns = back ? kColumns[t] : kColumns[t] / 2;
+    const int64_t tiles = (rows + kRows[t] - 1) / kRows[t] * ((n + columns - 1) / columns);
+    const double slower = !ragged || dtype == kF32 ? 1.0 : t == kLarge ? 1.15 : 1.45;
+    for (int s = 1; s <= 32 && (s == 1 || 4 * s <= steps); s += s < 4 ? 1 : s / 2) {
+      const int64_t groups = tiles * s, full = groups / (kCUs * kPerCU[t]);
+      const int64_t rest = groups - full * kCUs * kPerCU[t], long_part = (steps + s - 1) / s;
+      const double* step = dtype == kF32 ? kStep32[t] : kStep16[t];
+      double us = full * (long_part * step[kPerCU[t] - 1] * slower + kRound[t]);
+      if (rest) {
+        const double one = t == kLarge && groups <= kCUs / 2 ? 1.15 : step[(rest + kCUs - 1) / kCUs - 1];
+        us += long_part * one * slower + kRound[t];
+      }
+      if (s > 1) us += 4.0 + 0.25 * s + 2.0 * 4.0 * s * (double)rows * n * (back ? 1 : 2) / 5e6;
+      if (us < least) {
+        least = us;
+        best = {(TileKind)t, s};
+      }
+    }
+  }
+  return best;
+}
+
+int64_t workspace_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
+  if (rows == 0 || n == 0) return 0;
+  const int s = shape_of(rows, n, depth, back, dtype).splits;
+  return s > 1 ? (int64_t)s * (back ? 1 : 2) * rows * n * 4 : 0;
 }
 
 template <int DT, bool BACK, int ACT>
-hipError_t product(const Product& g, hipStream_t st) {
-  constexpr int kSize = sizeof(typename Elt<DT>::T);
-  const int width_b = BACK ? g.n : g.depth;
-  if (whole_pieces(g.a[0], g.depth, kSize) && (!BACK || whole_pieces(g.a[1], g.depth, kSize)) &&
-      whole_pieces(g.b[0], width_b, kSize) && whole_pieces(g.b[1], width_b, kSize)) {
-    typedef DirectTile<DT, BACK, 256, 256, 2, 4> C;
-    const int64_t tiles = (g.rows + C::kBM - 1) / C::kBM * ((g.n + C::kCols - 1) / C::kCols);
-    k_product_direct<DT, BACK, C, ACT><<<(unsigned)tiles, C::kThreads, 0, st>>>(g);
-    return hipGetLastError();
+hipError_t product(Product g, hipStream_t st) {
+  const Shape s = shape_of(g.rows, g.n, g.depth, BACK, DT);
+  g.splits = s.splits;
+  hipError_t e = hipSuccess;
+  if (s.tile == kLarge) {
+    if constexpr (DT != kF32) e = product<DT, BACK, ACT, Large<DT, BACK>>(g, st);
+  } else if (s.tile == kSmall) {
+    e = product<DT, BACK, ACT, Small<DT, BACK>>(g, st);
+  } else {
+    e = product<DT, BACK, ACT, Tiny<DT, BACK>>(g, st);
   }
-  typedef Tile<DT, BACK, 128, 128, 2, 2> C;
-  const int64_t tiles = (g.rows + C::kBM - 1) / C::kBM * ((g.n + C::kCols - 1) / C::kCols);
-  k_product<DT, BACK, C, ACT><<<(unsigned)tiles, C::kThreads, 0, st>>>(g);
+  if (e || g.splits == 1) return e;
+  k_product_join<DT, BACK, ACT><<<blocks_for(g.rows * ((g.n + 7) / 8), 256), 256, 0, st>>>(g);
   return hipGetLastError();
 }
 
@@ -550,13 +682,11 @@ hipError_t slope(const GatedGradArgs& a, hipStream_t st) {
 }  // namespace
 
 int64_t gated_workspace(int64_t rows, int32_t n, int32_t cols, int dtype) {
-  (void)rows, (void)n, (void)cols, (void)dtype;
-  return 0;
+  return workspace_of(rows, n, cols, false, dtype);
 }
 
 int64_t gated_grad_workspace(int64_t rows, int32_t n, int32_t cols, int dtype) {
-  (void)rows, (void)n, (void)cols, (void)dtype;
-  return 0;
+  return workspace_of(rows, cols, n, true, dtype);
 }
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
@@ -572,6 +702,7 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
   g.out[1] = a.gate;
   g.out[2] = a.up;
   g.act = a.act;
+  g.ws = static_cast<float*>(a.ws);
   return a.dtype == kF32    ? forward<kF32>(g, st)
          : a.dtype == kBF16 ? forward<kBF16>(g, st)
                             : forward<kF16>(g, st);
@@ -594,6 +725,7 @@ hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t st) {
   g.b[0] = a.w_gate;
   g.b[1] = a.w_up;
   g.out[0] = a.dx;
+  g.ws = static_cast<float*>(a.ws);
   return a.dtype == kF32    ? product<kF32, true, kSilu>(g, st)
          : a.dtype == kBF16 ? product<kBF16, true, kSilu>(g, st)
                             : product<kF16, true, kSilu>(g, st);
