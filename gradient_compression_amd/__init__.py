@@ -919,14 +919,15 @@ def gated_linear_backward(dh, gate, up, dgate, dup, w_gate=None, w_up=None, dx=N
 
 # ------------------------------------------------------------ the gradients of many tensors
 def _tensors(ts, name, dev):
-    """(pointers, sizes, type codes) of contiguous tensors, as host arrays."""
+    """(pointers, sizes, type codes) of contiguous tensors as host arrays, and the addresses of the
+    three."""
     Tensor, codes = _types[1], _types[2]
-    try:
-        ptrs = [t.data_ptr() for t in ts]
-        sizes = [t.numel() for t in ts]
-        kinds = [codes[t.dtype] for t in ts]
-        fine = all([t.is_contiguous() and t.get_device() == dev for t in ts])
-    except (AttributeError, KeyError, RuntimeError):
+    try:      # the shortest ways: a model has hundreds of them
+        ptrs = np.array(list(map(Tensor.data_ptr, ts)), np.uint64)
+        sizes = np.array(list(map(Tensor.numel, ts)), np.int64)
+        kinds = np.array([codes[t.dtype] for t in ts], np.int32)
+        fine = all(map(Tensor.is_contiguous, ts)) and set(map(Tensor.get_device, ts)) <= {dev}
+    except (AttributeError, KeyError, RuntimeError, TypeError):
         fine = False
     if not fine:      # say which
         for i, t in enumerate(ts):
@@ -937,13 +938,13 @@ def _tensors(ts, name, dev):
             if not t.is_contiguous():
                 raise ValueError(f"{name}[{i}] must be contiguous")
         raise TypeError(f"{name} must be strided tensors")
-    return (np.array(ptrs, np.uint64), np.array(sizes, np.int64), np.array(kinds, np.int32))
+    return ptrs, sizes, kinds, (ptrs.ctypes.data, sizes.ctypes.data, kinds.ctypes.data)
 
 
 def _outputs(out, arrays, tensors, dev):
     """(pointers, type codes, tensors) of what the tensors are scaled into: themselves, as many
     tensors, or one tensor that they are laid into back to back."""
-    ptrs, sizes, kinds = arrays
+    ptrs, sizes, kinds, _ = arrays
     if out is None:
         return ptrs, kinds, tensors
     if isinstance(out, _types[1]):
@@ -965,26 +966,22 @@ def _scalar(t, name, dev):
 
 
 def _grad_norm(arrays, norm, norms, workspace, stream, dev):
-    ptrs, sizes, kinds = arrays
-    n, L = len(sizes), lib()
+    at = arrays[3]
+    n, L = len(arrays[1]), lib()
     need = ctypes.c_int64()
-    _check(L.gc_grad_norm_workspace(_np_ptr(sizes), n, ctypes.byref(need)),
-           "gc_grad_norm_workspace")
+    _check(L.gc_grad_norm_workspace(at[1], n, ctypes.byref(need)), "gc_grad_norm_workspace")
     ws, ws_bytes, _keep = _workspace(workspace, need.value, stream, dev)
-    _check(L.gc_grad_norm(_np_ptr(ptrs), _np_ptr(sizes), _np_ptr(kinds), n,
-                          _scalar(norm, "norm", dev),
+    _check(L.gc_grad_norm(*at, n, _scalar(norm, "norm", dev),
                           _array(norms, "norms", _types[0].float32, n, dev), ws, ws_bytes,
                           _raw_stream(stream, dev)), "gc_grad_norm")
     _types[4]((norm,) if norms is None else (norm, norms))
 
 
 def _grad_clip(arrays, tensors, max_norm, norm, out, factors, stream, dev):
-    ptrs, sizes, kinds = arrays
     to, to_kinds, written = _outputs(out, arrays, tensors, dev)
     f = 0 if factors is None else factors.numel()
-    _check(lib().gc_grad_clip(_np_ptr(ptrs), _np_ptr(sizes), _np_ptr(kinds), len(sizes),
-                              _np_ptr(to), _np_ptr(to_kinds), float(max_norm),
-                              _scalar(norm, "norm", dev),
+    _check(lib().gc_grad_clip(*arrays[3], len(arrays[1]), to.ctypes.data, to_kinds.ctypes.data,
+                              float(max_norm), _scalar(norm, "norm", dev),
                               _array(factors, "factors", _types[0].float32, f, dev), f,
                               _raw_stream(stream, dev)), "gc_grad_clip")
     _types[4](list(written) if factors is None else [*written, factors])

@@ -43,7 +43,9 @@ hipError_t launch_grad_squares(const NormTable& t, double* sums, GradSums* of, u
 // norm = sqrt of all `total` sums; norms[t] (where given) = sqrt of tensor t's.
 hipError_t launch_grad_roots(const double* sums, uint32_t total, const GradSums* of, int32_t n,
                              float* norm, float* norms, hipStream_t st);
-hipError_t launch_grad_clip(const ClipTable& t, float max_norm, const float* norm, hipStream_t st);
+// stream: what is written is more than the cache holds.
+hipError_t launch_grad_clip(const ClipTable& t, bool stream, float max_norm, const float* norm,
+                            hipStream_t st);
 hipError_t launch_grad_factors(float max_norm, const float* norm, float* factors, int64_t n,
                                hipStream_t st);
 

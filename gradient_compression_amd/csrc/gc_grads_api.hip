@@ -14,6 +14,10 @@ namespace {
 
 constexpr int64_t kMostElements = (int64_t)1 << 44;   // of a tensor, and of a call
 constexpr int32_t kMostTensors = 1 << 20;
+// Results of more than this are stored non-temporally, as no cache would keep them for their reader and the
+// tensors stay in it instead: 391 tensors of 335 M elements into fp32 540 us in place of 562, 2^30 elements
+// 1596 in place of 1636.
+constexpr int64_t kCache = (int64_t)256 << 20;
 
 bool valid_dtype(int32_t d) { return d == GC_F32 || d == GC_BF16 || d == GC_F16; }
 int64_t size_of(int32_t d) { return d == GC_F32 ? 4 : 2; }
@@ -41,41 +45,30 @@ bool valid_tensors(const void* const* p, const int64_t* sizes, const int32_t* dt
   return true;
 }
 
-// A piece of memory that a call reads or writes; `of`: the tensor that it is, or -1.
+// A piece of memory that a call reads or writes.
 struct Piece {
   uintptr_t begin, end;
-  int32_t of;
   bool out;
 };
 
-void add(std::vector<Piece>& v, const void* p, int64_t bytes, int32_t of, bool out) {
+Piece piece(const void* p, int64_t bytes, bool out) {
   const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-  if (p && bytes > 0) v.push_back({b, b + (uintptr_t)bytes, of, out});
+  return {b, b + (p ? (uintptr_t)bytes : 0), out};
 }
 
-// True when an output shares a byte with another piece, but for an output that is its own tensor.
+bool meet(const Piece& a, const Piece& b) {   // share a byte
+  return a.begin < b.end && b.begin < a.end;
+}
+
+// True when an output shares a byte with another piece.
 bool clash(std::vector<Piece>& v) {
-  std::sort(v.begin(), v.end(),
-            [](const Piece& a, const Piece& b) { return a.begin < b.begin; });
-  // the pieces so far that reach farthest: of the outputs, and of the inputs
-  const Piece* out = nullptr;
-  const Piece* in = nullptr;
-  const Piece* in2 = nullptr;   // the farthest input of another tensor than `in`
-  auto meet = [](const Piece* a, const Piece& b) {
-    return a && a->end > b.begin &&
-           !(a->of >= 0 && a->of == b.of && a->out != b.out && a->begin == b.begin &&
-             a->end == b.end);
-  };
+  auto before = [](const Piece& a, const Piece& b) { return a.begin < b.begin; };
+  if (!std::is_sorted(v.begin(), v.end(), before)) std::sort(v.begin(), v.end(), before);
+  const Piece *out = nullptr, *in = nullptr;   // the pieces so far that reach farthest
   for (const Piece& p : v) {
-    if (meet(out, p) || (p.out && (meet(in, p) || meet(in2, p)))) return true;
-    if (p.out) {
-      if (!out || p.end > out->end) out = &p;
-    } else if (!in || p.end > in->end) {
-      if (in && in->of != p.of) in2 = in;
-      in = &p;
-    } else if (p.of != in->of && (!in2 || p.end > in2->end)) {
-      in2 = &p;
-    }
+    if ((out && meet(*out, p)) || (p.out && in && meet(*in, p))) return true;
+    const Piece*& far = p.out ? out : in;
+    if (!far || p.end > far->end) far = &p;
   }
   return false;
 }
@@ -141,16 +134,14 @@ int gc_grad_norm(const void* const* tensors, const int64_t* sizes, const int32_t
   if (!valid_tensors(tensors, sizes, dtypes, n) || !norm || !aligned(norm, 4) ||
       !aligned(norms, 4) || workspace_bytes < need || (need && !workspace) || !aligned(workspace, 16))
     return GC_ERR_INVALID_ARG;
-  try {
-    std::vector<Piece> v;
-    v.reserve(n + 3);
-    for (int32_t t = 0; t < n; ++t) add(v, tensors[t], sizes[t] * size_of(dtypes[t]), t, false);
-    add(v, norm, 4, -1, true);
-    add(v, norms, (int64_t)n * 4, -1, true);
-    add(v, workspace, need, -1, true);
-    if (clash(v)) return GC_ERR_INVALID_ARG;
-  } catch (const std::bad_alloc&) {
-    return GC_ERR_OOM;
+  const Piece outs[3] = {piece(norm, 4, true), piece(norms, (int64_t)n * 4, true),
+                         piece(workspace, need, true)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(outs[j], outs[i])) return GC_ERR_INVALID_ARG;
+    for (int32_t t = 0; t < n; ++t)
+      if (meet(piece(tensors[t], sizes[t] * size_of(dtypes[t]), false), outs[i]))
+        return GC_ERR_INVALID_ARG;
   }
   const hipStream_t st = static_cast<hipStream_t>(stream);
   double* sums = static_cast<double*>(workspace);
@@ -181,19 +172,26 @@ int gc_grad_clip(const void* const* tensors, const int64_t* sizes, const int32_t
   try {
     std::vector<Piece> v;
     v.reserve(2 * (size_t)n + 2);
+    auto add = [&](const Piece& p) {
+      if (p.end > p.begin) v.push_back(p);
+    };
     for (int32_t t = 0; t < n; ++t) {
-      // an output in its tensor's place has to be of its type: then the two pieces are alike
-      add(v, tensors[t], sizes[t] * size_of(dtypes[t]), t, false);
-      add(v, out[t], sizes[t] * size_of(out_dtypes[t]), t, true);
-      if (sizes[t] && out[t] == tensors[t] && out_dtypes[t] != dtypes[t]) return GC_ERR_INVALID_ARG;
+      // an output in its tensor's place has to be of its type: then the two are one piece
+      if (out[t] != tensors[t])
+        add(piece(tensors[t], sizes[t] * size_of(dtypes[t]), false));
+      else if (sizes[t] && out_dtypes[t] != dtypes[t])
+        return GC_ERR_INVALID_ARG;
+      add(piece(out[t], sizes[t] * size_of(out_dtypes[t]), true));
     }
-    add(v, norm, 4, -1, false);
-    add(v, factors, n_factors * 4, -1, true);
+    add(piece(norm, 4, false));
+    add(piece(factors, n_factors * 4, true));
     if (clash(v)) return GC_ERR_INVALID_ARG;
   } catch (const std::bad_alloc&) {
     return GC_ERR_OOM;
   }
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  int64_t written = 0;
+  for (int32_t t = 0; t < n; ++t) written += sizes[t] * size_of(out_dtypes[t]);
   hipError_t e = each_launch(
       sizes, n, gc::kClipTensors, [&](int32_t first, int32_t count, int64_t chunks) -> hipError_t {
         if (!chunks) return hipSuccess;
@@ -204,7 +202,7 @@ int gc_grad_clip(const void* const* tensors, const int64_t* sizes, const int32_t
           t.tail[i] |= (uint32_t)out_dtypes[first + i] << 18 |
                        (uint32_t)(out[first + i] == tensors[first + i]) << 20;
         }
-        return gc::launch_grad_clip(t, max_norm, norm, st);
+        return gc::launch_grad_clip(t, written > kCache, max_norm, norm, st);
       });
   if (e == hipSuccess && n_factors)
     e = gc::launch_grad_factors(max_norm, norm, factors, n_factors, st);
