@@ -138,36 +138,45 @@ struct Product {
 constexpr int kChunk = 16, kRowBytes = 128, kRowChunks = kRowBytes / kChunk;
 
 // A workgroup's tile, BM rows by BN columns (forward: BN / 2 of each projection), shared by WM x WN
-// waves.  A step sums 128 bytes of a row.
-template <int DT, bool BACK, int BM, int BN, int WM, int WN>
+// waves.  A step sums 128 bytes of a row.  PARTS (1, or 3 of fp32): the bf16 values whose sum an element is
+// in LDS.
+template <int DT, bool BACK, int BM, int BN, int WM, int WN, int PARTS = 1>
 struct Tile {
   typedef typename Elt<DT>::T T;
+  typedef Tile<DT, BACK, BM, BN, WM, WN> Whole;   // without parts
+  static constexpr int kParts = PARTS;
   static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN;
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int kFM = BM / WM / 32, kFN = BN / WN / 32;
   static constexpr int kElts = kChunk / (int)sizeof(T), kBK = kRowChunks * kElts;
   static constexpr int kCols = BACK ? BN : BN / 2;      // of the result
   static constexpr int kPiecesB = BACK ? BN / kElts : kRowChunks;   // of a row of the second operand
-  static constexpr int kPitchB = kPiecesB * kChunk;
-  static constexpr int kBytesA = BM * kRowBytes, kBytesB = (BACK ? kBK : BN) * kPitchB;
+  // In LDS: rows of the summed dimension, or of BN columns (one part after the other).
+  static constexpr int kPitch = PARTS == 1 ? kRowBytes : PARTS * kRowBytes / 2;
+  static constexpr int kPitchB = !BACK ? kPitch : PARTS == 1 ? kPiecesB * kChunk : BN * 2;
+  static constexpr int kBytesA = BM * kPitch, kBytesB = BACK ? PARTS * kBK * kPitchB : BN * kPitchB;
   static constexpr int kStage = kBytesA + kBytesB;
+  static constexpr int kSlices = PARTS == 1 ? kRowChunks / 2 : kBK / 16;   // of a step, each one product deep
   // Loading: an item is one piece a thread, kRowsA rows of a step's first or kRowsB of its second operand.
   static constexpr int kRowsA = kThreads / kRowChunks, kRowsB = kThreads / kPiecesB;
-  static constexpr int kItemsA = kBytesA / kChunk / kThreads, kItemsB = kBytesB / kChunk / kThreads;
+  static constexpr int kItemsA = BM * kRowChunks / kThreads;
+  static constexpr int kItemsB = (BACK ? kBK : BN) * kPiecesB / kThreads;
   static_assert(BN >= 128 && (BACK || (kFN % 2 == 0 && kRowsB % 16 == 0 && kRowsB <= 64)), "layouts");
 };
 
 // Where 16-byte piece c of row r of a tile lies: the pieces of 16 neighbouring rows that a read takes
-// at once fall into different banks.
-__device__ __forceinline__ int piece_at(int r, int c) {
-  return r * kRowBytes + ((c ^ ((r >> 1) & (kRowChunks - 1))) * kChunk);
+// at once fall into different banks.  With parts, piece c (of 4) of part q.
+template <int PARTS>
+__device__ __forceinline__ int piece_at(int r, int c, int q = 0) {
+  if (PARTS == 1) return r * kRowBytes + ((c ^ ((r >> 1) & (kRowChunks - 1))) * kChunk);
+  return (r * PARTS + q) * (kRowBytes / 2) + ((c ^ ((r >> 2) & 3)) * kChunk);
 }
 
 // Where the 64-byte block b of row r lies in a row of the backward pass's second operand: the four rows
-// of a transposing read (fp32: the two halves of a wave, four rows apart) in different banks.
-template <int DT>
+// of a transposing read (whole fp32: the two halves of a wave, four rows apart) in different banks.
+template <bool WIDE>
 __device__ __forceinline__ int block_at(int r, int b) {
-  return DT == kF32 ? b ^ ((r >> 1) & 2) : b ^ (r & 3);
+  return WIDE ? b ^ ((r >> 1) & 2) : b ^ (r & 3);
 }
 
 // The column (of 32) that row i of a product's first operand stands for: a lane's 16 registers hold
@@ -199,6 +208,24 @@ __device__ __forceinline__ u4 load_piece(const T* p, int k, int end) {
     }
   }
   return k < end ? u4{d[0], d[1], d[2], d[3]} : u4{};
+}
+
+// The three bf16 values whose sum each of 4 fp32 is, each the nearest to what the ones before it leave (8 bits
+// of 24).  Inf and NaN, and what rounds to Inf, leave NaN.
+__device__ __forceinline__ void parts_of(const u4& w, u2 (&part)[3]) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float a = __uint_as_float(w[2 * h]), b = __uint_as_float(w[2 * h + 1]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const uint32_t t = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf2));
+      part[q][h] = t;
+      a -= __uint_as_float(t << 16);
+      b -= __uint_as_float(t & 0xFFFF0000u);
+    }
+  }
 }
 
 // acc += a b for 16 bytes of the summed dimension a lane.
@@ -311,26 +338,28 @@ __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int* tm, int* 
   *tn = in / high;
 }
 
-template <int DT, bool BACK, typename C, int ACT>
-__global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
+// A workgroup's tile from row m0 and column n0 on: `steps` steps of the sum from `first` on.
+template <int DT, bool BACK, typename C>
+__device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t m0, int n0, int first,
+                                         int steps, f16v (&acc)[C::kFM][C::kFN]) {
   typedef typename Elt<DT>::T T;
-  constexpr int E = C::kElts, kItems = C::kItemsA + C::kItemsB, kSlices = kRowChunks / 2;
+  constexpr int E = C::kElts, kItems = C::kItemsA + C::kItemsB, kSlices = C::kSlices;
+  constexpr int P = C::kParts;
+  constexpr bool kWide = DT == kF32 && P == 1;
   constexpr int64_t kSize = sizeof(T);
-  __shared__ __align__(16) char s_mem[2 * C::kStage];
-  int tm, tn;
-  tile_of((int)((g.rows + C::kBM - 1) / C::kBM), (g.n + C::kCols - 1) / C::kCols, &tm, &tn);
-  const int64_t m0 = (int64_t)tm * C::kBM;
-  const int n0 = tn * C::kCols;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int wm = wave / C::kWN * (C::kFM * 32), wn = wave % C::kWN * (C::kFN * 32);
-  const int steps_seg = (g.depth + C::kBK - 1) / C::kBK, all_steps = (BACK ? 2 : 1) * steps_seg;
-  const int first = (int)((int64_t)all_steps * blockIdx.y / g.splits);
-  const int steps = (int)((int64_t)all_steps * (blockIdx.y + 1) / g.splits) - first;
+  const int steps_seg = (g.depth + C::kBK - 1) / C::kBK;
 
   // This thread's piece of every item: A's row p * kRowsA + ra, piece ca of the step; B's likewise.
-  const int ra = threadIdx.x / kRowChunks, ca = (threadIdx.x % kRowChunks) ^ ((ra >> 1) & 7);
+  // Whole elements lie in the order of the threads, so that the piece is the one which belongs there; parts
+  // find their places when they are stored.
+  const int ra = threadIdx.x / kRowChunks, sa = threadIdx.x % kRowChunks;
   const int rb = threadIdx.x / C::kPiecesB, sb = threadIdx.x % C::kPiecesB;
-  const int cb = BACK ? block_at<DT>(rb, sb >> 2) * 4 + (sb & 3) : sb ^ ((rb >> 1) & 7);
+  const int ca = P > 1 ? sa : sa ^ ((ra >> 1) & 7);
+  const int cb = P > 1  ? sb
+                 : BACK ? block_at<kWide>(rb, sb >> 2) * 4 + (sb & 3)
+                        : sb ^ ((rb >> 1) & 7);
   // Where the rows of the items lie from the tile's first (rows past the last one read it; what they add
   // up is not stored).
   auto row_a = [&](int p) { return min(m0 + p * C::kRowsA + ra, g.rows - 1) - m0; };
@@ -392,8 +421,26 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
       if (BACK && row_b(b) >= left) reg[p] = u4{};
     }
   };
-  auto store = [&](char* stage, int p) {
-    *reinterpret_cast<u4*>(stage + (p * C::kThreads + threadIdx.x) * kChunk) = reg[p];
+  auto store = [&](char* stage, int p, const u4& w) {
+    if constexpr (P == 1) {
+      *reinterpret_cast<u4*>(stage + (p * C::kThreads + threadIdx.x) * kChunk) = w;
+    } else {
+      u2 part[3];
+      parts_of(w, part);
+#pragma unroll
+      for (int q = 0; q < P; ++q) {
+        const int b = p - C::kItemsA;
+        char* to = stage;
+        if (p < C::kItemsA)
+          to += piece_at<P>(p * C::kRowsA + ra, ca >> 1, q) + (ca & 1) * 8;
+        else if (!BACK)
+          to += C::kBytesA + piece_at<P>(b * C::kRowsB + rb, cb >> 1, q) + (cb & 1) * 8;
+        else
+          to += C::kBytesA + (q * C::kBK + b * C::kRowsB + rb) * C::kPitchB +
+                block_at<false>(rb, cb >> 3) * 64 + (cb & 7) * 8;
+        *reinterpret_cast<u2*>(to) = part[q];
+      }
+    }
   };
   // Steps that can be loaded whole from here on: none where the offsets in a tile pass 32 bits.  (A piece
   // that starts inside a row of the backward pass's weight but ends behind it reads on into the next row,
@@ -405,32 +452,34 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
   };
 
   const int half = lane >> 5, in = lane & 31;
-  auto read_a = [&](const char* stage, int s, u4 (&f)[C::kFM]) {
+  auto read_a = [&](const char* stage, int s, u4 (&f)[P][C::kFM]) {
 #pragma unroll
-    for (int i = 0; i < C::kFM; ++i)
-      f[i] = *reinterpret_cast<const u4*>(stage + piece_at(wm + 32 * i + in, 2 * s + half));
+    for (int q = 0; q < P; ++q)
+#pragma unroll
+      for (int i = 0; i < C::kFM; ++i)
+        f[q][i] = *reinterpret_cast<const u4*>(stage + piece_at<P>(wm + 32 * i + in, 2 * s + half, q));
   };
-  auto read_b = [&](const char* stage, int s, u4 (&f)[C::kFN]) {
-    const char* q = stage + C::kBytesA;
+  auto read_b = [&](const char* stage, int s, u4 (&f)[P][C::kFN]) {
 #pragma unroll
-    for (int j = 0; j < C::kFN; ++j) {
+    for (int t = 0; t < P * C::kFN; ++t) {
+      const int q = t / C::kFN, j = t % C::kFN;
+      const char* from = stage + C::kBytesA + (BACK ? q * C::kBK * C::kPitchB : 0);
       if constexpr (!BACK) {
-        f[j] = *reinterpret_cast<const u4*>(q + piece_at(wn + 32 * j + in, 2 * s + half));
-      } else if constexpr (DT == kF32) {
+        f[q][j] = *reinterpret_cast<const u4*>(from + piece_at<P>(wn + 32 * j + in, 2 * s + half, q));
+      } else if constexpr (kWide) {
         const int r = (2 * s + half) * E, c = (wn + 32 * j) * 4 + column_of(in) * 4;
-        const char* t = q + r * C::kPitchB + block_at<DT>(r, c >> 6) * 64 + (c & 63);
+        from += r * C::kPitchB + block_at<kWide>(r, c >> 6) * 64 + (c & 63);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          f[j][e] = *reinterpret_cast<const uint32_t*>(t + e * C::kPitchB);
+          f[q][j][e] = *reinterpret_cast<const uint32_t*>(from + e * C::kPitchB);
       } else {
         // four rows of 16 columns for 16 lanes; the lanes' groups of 4 columns in the products' order
         const int group = 4 * ((lane >> 4) & 1) + (lane & 3), r4 = (lane & 15) >> 2;
-        const char* t = q + ((2 * s + half) * E + r4) * C::kPitchB +
-                        block_at<DT>(r4, (wn + 32 * j) >> 5) * 64 +
-                        (16 * (group & 1) + 4 * (group >> 1)) * 2;
-        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)t);
-        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(t + 4 * C::kPitchB));
-        f[j] = __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        from += ((2 * s + half) * 8 + r4) * C::kPitchB + block_at<kWide>(r4, (wn + 32 * j) >> 5) * 64 +
+                (16 * (group & 1) + 4 * (group >> 1)) * 2;
+        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)from);
+        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(from + 4 * C::kPitchB));
+        f[q][j] = __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
     }
   };
@@ -446,9 +495,12 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
     advance();
   };
 
-  f16v acc[C::kFM][C::kFN] = {};
+#pragma unroll
+  for (int i = 0; i < C::kFM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::kFN; ++j) acc[i][j] = f16v{};
   char *cur = s_mem, *nxt = s_mem + C::kStage;
-  u4 fa[C::kFM], fb[C::kFN];
+  u4 fa[P][C::kFM], fb[P][C::kFN];
   if (steps > 0) {
     start(first >= steps_seg, first >= steps_seg ? first - steps_seg : first);
     if (steps > 1 && whole_steps() > 1) {   // both steps' loads on their way at once
@@ -463,12 +515,11 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
       }
       advance();
 #pragma unroll
-      for (int p = 0; p < kItems; ++p)
-        *reinterpret_cast<u4*>(cur + (p * C::kThreads + threadIdx.x) * kChunk) = ahead[p];
+      for (int p = 0; p < kItems; ++p) store(cur, p, ahead[p]);
     } else {
       load_step();
 #pragma unroll
-      for (int p = 0; p < kItems; ++p) store(cur, p);
+      for (int p = 0; p < kItems; ++p) store(cur, p, reg[p]);
       if (steps > 1) load_step();
     }
     __syncthreads();
@@ -483,33 +534,42 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
   auto multiply_step = [&](auto load) {
 #pragma unroll
     for (int s = 0; s < kSlices; ++s) {
-      u4 na[C::kFM], nb[C::kFN];
+      u4 na[P][C::kFM], nb[P][C::kFN];
       if (s + 1 == kSlices) __syncthreads();
       read_b(s + 1 < kSlices ? cur : nxt, (s + 1) % kSlices, nb);
       read_a(s + 1 < kSlices ? cur : nxt, (s + 1) % kSlices, na);
 #pragma unroll
       for (int p = 0; p < kItems; ++p)
         if (p * (kSlices - 1) / kItems == s) {
-          store(nxt, p);
+          store(nxt, p, reg[p]);
           if (load) load_whole(p);
         }
+      // all pairs of parts but those below 2^-23 of the product, the smallest first
 #pragma unroll
-      for (int i = 0; i < C::kFM; ++i)
+      for (int d = P - 1; d >= 0; --d)
 #pragma unroll
-        for (int j = 0; j < C::kFN; ++j) multiply<DT>(fb[j], fa[i], acc[i][j]);
+        for (int q = 0; q <= d; ++q)
+#pragma unroll
+          for (int i = 0; i < C::kFM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::kFN; ++j)
+              multiply<P == 1 ? DT : kBF16>(fb[q][j], fa[d - q][i], acc[i][j]);
       // each matrix instruction followed by a share of the rest, which runs beside it
 #pragma unroll
-      for (int u = 0; u < C::kFM * C::kFN; ++u) {
-        __builtin_amdgcn_sched_group_barrier(0x008, DT == kF32 ? 4 : 1, 0);   // matrix
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                    // LDS reads
-        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                    // vector
-        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                    // loads
-        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);                    // LDS writes
+      for (int u = 0; u < C::kFM * C::kFN * P * (P + 1) / 2; ++u) {
+        __builtin_amdgcn_sched_group_barrier(0x008, kWide ? 4 : 1, 0);   // matrix
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);               // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x002, P == 1 ? 4 : 8, 0);  // vector
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);               // loads
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);               // LDS writes
       }
 #pragma unroll
-      for (int i = 0; i < C::kFM; ++i) fa[i] = na[i];
+      for (int q = 0; q < P; ++q) {
 #pragma unroll
-      for (int j = 0; j < C::kFN; ++j) fb[j] = nb[j];
+        for (int i = 0; i < C::kFM; ++i) fa[q][i] = na[q][i];
+#pragma unroll
+        for (int j = 0; j < C::kFN; ++j) fb[q][j] = nb[q][j];
+      }
     }
     if (load) advance();
     char* t = cur;
@@ -524,6 +584,43 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
     if (BACK && left <= 0 && seg == 0 && step + 2 < steps) continue;
     multiply_step(std::false_type());
     if (step + 1 < steps) load_step();   // the step after the next: step is one further now
+  }
+}
+
+template <int DT, bool BACK, typename C, int ACT>
+__global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
+  __shared__ __align__(16) char s_mem[2 * C::kStage];
+  int tm, tn;
+  tile_of((int)((g.rows + C::kBM - 1) / C::kBM), (g.n + C::kCols - 1) / C::kCols, &tm, &tn);
+  const int64_t m0 = (int64_t)tm * C::kBM;
+  const int n0 = tn * C::kCols;
+  const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+  const int wm = wave / C::kWN * (C::kFM * 32), wn = wave % C::kWN * (C::kFN * 32);
+  const int all = (BACK ? 2 : 1) * ((g.depth + C::kBK - 1) / C::kBK);
+  const int first = (int)((int64_t)all * blockIdx.y / g.splits);
+  const int steps = (int)((int64_t)all * (blockIdx.y + 1) / g.splits) - first;
+  f16v acc[C::kFM][C::kFN];
+  sum_tile<DT, BACK, C>(g, s_mem, m0, n0, first, steps, acc);
+  if constexpr (C::kParts > 1) {
+    // Parts do not multiply Inf (and what rounds to it) as it is: where NaN came out, the sum of whole
+    // elements says what it is.
+    bool nan = false;
+    auto each = [&](auto&& f) {
+#pragma unroll
+      for (int i = 0; i < C::kFM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::kFN; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) f(i, j, r);
+    };
+    each([&](int i, int j, int r) { nan |= acc[i][j][r] != acc[i][j][r]; });
+    if (__syncthreads_or(nan)) {
+      f16v whole[C::kFM][C::kFN];
+      sum_tile<DT, BACK, typename C::Whole>(g, s_mem, m0, n0, first, steps, whole);
+      each([&](int i, int j, int r) {
+        if (acc[i][j][r] != acc[i][j][r]) acc[i][j][r] = whole[i][j][r];
+      });
+    }
   }
   // each wave's own part of LDS, which all have stopped reading
   constexpr int kPart = 2 * C::kStage / (C::kThreads / 64);
@@ -570,6 +667,74 @@ __global__ __launch_bounds__(256) void k_product_join(Product g) {
   put(g.out[0], v);
 }
 
+// ------------------------------------------------------------------ few rows
+// The forward pass of up to 32 rows, as in serving: the weights are read once and everything else is small.
+// A workgroup forms 16 columns of each projection, which are the 32 rows of one operand; its 8 waves share
+// the sum, 128 bytes of the rows at a time, each operand straight from memory, and join their parts in
+// LDS: many workgroups, no second launch.  One row through 4096 x 1024 bf16 takes 4.3 us of the GPU (tiles
+// 8.6), through 11008 x 4096 31 (5.8 TB/s; 32.5).
+constexpr int kFewRows = 32, kFewWaves = 8, kFewColumns = 16;
+
+template <int DT, int ACT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(Product g) {
+  typedef typename Elt<DT>::T T;
+  constexpr int E = kChunk / sizeof(T), kDeep = kRowChunks * E, kPieces = kRowChunks / 2;
+  __shared__ float s_sum[kFewWaves][32][33];   // 33: the columns of a row in different banks
+  const int lane = lane_id(), wave = wave_id(), half = lane >> 5, in = lane & 31;
+  const int n0 = blockIdx.x * kFewColumns;
+  const Mat& w = g.b[in >> 4];
+  const T* pw = static_cast<const T*>(w.p) + min(n0 + (in & 15), g.n - 1) * w.ld;
+  const T* px = static_cast<const T*>(g.a[0].p) + min((int64_t)in, g.rows - 1) * g.a[0].ld;
+  f16v acc = {};
+  u4 fw[kPieces], fx[kPieces];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int k = k0 + (2 * j + half) * E;
+      if (k0 + kDeep <= g.depth) {
+        fw[j] = *reinterpret_cast<const u4_at_any*>(pw + k);
+        fx[j] = *reinterpret_cast<const u4_at_any*>(px + k);
+      } else {
+        fw[j] = load_piece(pw, k, g.depth);
+        fx[j] = load_piece(px, k, g.depth);
+      }
+    }
+  };
+  int k0 = wave * kDeep;
+  if (k0 < g.depth) load(k0);
+  while (k0 < g.depth) {
+    u4 cw[kPieces], cx[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      cw[j] = fw[j];
+      cx[j] = fx[j];
+    }
+    k0 += kFewWaves * kDeep;
+    if (k0 < g.depth) load(k0);
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) multiply<DT>(cw[j], cx[j], acc);
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s_sum[wave][8 * (r >> 2) + 4 * half + (r & 3)][in] = acc[r];
+  __syncthreads();
+  static_assert(64 * kFewWaves == kFewRows * kFewColumns, "a thread for each result");
+  const int i = threadIdx.x % kFewColumns, row = threadIdx.x / kFewColumns, col = n0 + i;
+  if (col >= g.n || row >= g.rows) return;
+  float v[1] = {}, u[1] = {};
+#pragma unroll
+  for (int k = 0; k < kFewWaves; ++k) {
+    v[0] += s_sum[k][i][row];
+    u[0] += s_sum[k][16 + i][row];
+  }
+  auto put = [&](const Mat& m, float x) {
+    static_cast<T*>(m.p)[row * m.ld + col] = round_to<DT>(x);
+  };
+  if (g.out[1].p) put(g.out[1], v[0]);
+  if (g.out[2].p) put(g.out[2], u[0]);
+  gate<ACT, 1>(v, u);
+  put(g.out[0], v[0]);
+}
+
 template <int DT, bool BACK, int ACT, typename C>
 hipError_t product(const Product& g, hipStream_t st) {
   const int64_t tiles = (g.rows + C::kBM - 1) / C::kBM * ((g.n + C::kCols - 1) / C::kCols);
@@ -578,13 +743,14 @@ hipError_t product(const Product& g, hipStream_t st) {
 }
 
 template <int DT, bool BACK>
-using Large = Tile<DT, BACK, 256, 256, 2, 4>;
+using Large = std::conditional_t<DT == kF32, Tile<DT, BACK, 256, 128, 4, 2, 3>,
+                                 Tile<DT, BACK, 256, 256, 2, 4>>;
 template <int DT, bool BACK>
-using Small = Tile<DT, BACK, 128, 128, 2, 2>;
+using Small = Tile<DT, BACK, 128, 128, 2, 2, DT == kF32 ? 3 : 1>;
 template <int DT, bool BACK>
-using Tiny = Tile<DT, BACK, 64, 128, 2, 2>;
+using Tiny = Tile<DT, BACK, 64, 128, 2, 2, DT == kF32 ? 3 : 1>;
 
-enum TileKind { kLarge, kSmall, kTiny };
+enum TileKind { kLarge, kSmall, kTiny, kFew };   // kFew: the forward pass of few rows
 
 struct Shape {
   TileKind tile;
@@ -594,39 +760,54 @@ struct Shape {
 // A large tile needs the fewest loads a product, but leaves CUs idle where the result is small; a long sum
 // can be split over CUs, at the price of writing and joining its parts.  The tile and the split with the
 // least estimated time are taken.  A step (64 summed columns of the 16-bit types, 32 of fp32) of a tile
-// takes, with 1, 2 and 3 workgroups on its CU, in microseconds (measured; a CU holds 1 large, 2 small or 3
-// tiny ones):
-//              large          small        tiny
-//   16 bits    1.15 or 1.72   0.53 1.0     0.50 0.69 1.05   (large: on up to half of the CUs, or all)
-//   fp32       -              1.95 3.84    1.1  2.1  3.2
+// takes, with 1, 2 and 3 workgroups on its CU, in microseconds (measured; a CU holds 1 large tile, of the
+// 16-bit types 2 small or 3 tiny ones, of fp32 1 and 2):
+//              large          small       tiny
+//   16 bits    1.15 or 1.72   0.53 1.0    0.50 0.69 1.05
+//   fp32       1.6 or 2.4     1.4         0.84 1.47         (large: on up to half of the CUs, or all)
 // and a round of tiles 14, 7 or 4 us besides (launch, first loads, the results' way); a join 4 us, 0.25 us a
-// part and their bytes (written and read) at 5 TB/s.  In fp32 a large tile gains 5 % over small ones.  Where the
-// rows' widths are not whole 16 bytes, as where they start anywhere, a large step takes 1.15 times and the
-// others 1.45 times as long.
+// part and their bytes (written and read) at 5 TB/s.  Where the 16-bit types' rows are not whole 16 bytes
+// wide, as where they start anywhere, a large step takes 1.15 times and the others 1.45 times as long.
+// Measured against every other choice over 50 drawn sizes, the rule's takes 5 % longer than the best.
+//
+// Up to 32 rows of a forward pass may go without tiles: 3.5 us, and 1.1 us (ragged 16-bit rows: 2.6) and a
+// little more with the rows for each 1 KB of a row's sum, with the workgroups in as many turns as fill the
+// CUs.  One row through 4096 x 4096 bf16 13.0 us (tiles 17.2), 3000 x 3001 19.4 (17.2), 1000 x 8000 19.2
+// (14.5); 32 rows through 4096 x 4096 16.9 (18.3), 11008 x 4096 44.4 (35.4).
 Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
-  constexpr int kRows[3] = {256, 128, 64}, kColumns[3] = {256, 128, 128}, kPerCU[3] = {1, 2, 3};
+  struct Costs {
+    int columns, per_cu[3], bk;
+    double few, step[3][3];
+  };
+  constexpr Costs k16 = {256, {1, 2, 3}, 64, 1.15, {{1.72}, {0.53, 1.0}, {0.50, 0.69, 1.05}}};
+  constexpr Costs k32 = {128, {1, 1, 2}, 32, 1.6, {{2.4}, {1.4}, {0.84, 1.47}}};
+  constexpr int kRows[3] = {256, 128, 64};
   constexpr double kRound[3] = {14.0, 7.0, 4.0};
-  constexpr double kStep16[3][3] = {{1.72}, {0.53, 1.0}, {0.50, 0.69, 1.05}};
-  constexpr double kStep32[3][3] = {{}, {1.95, 3.84}, {1.1, 2.1, 3.2}};
   constexpr int64_t kCUs = 256;
-  const int bk = dtype == kF32 ? 32 : 64;
-  const int64_t steps = (back ? 2 : 1) * (((int64_t)depth + bk - 1) / bk);
-  const bool ragged = depth % (bk / 8) || (back && n % (bk / 8));
+  const Costs& k = dtype == kF32 ? k32 : k16;
+  const int64_t steps = (back ? 2 : 1) * (((int64_t)depth + k.bk - 1) / k.bk);
+  const bool ragged = dtype != kF32 && (depth % 8 || (back && n % 8));
   Shape best = {kTiny, 1};
   double least = 1e300;
-  for (int t = dtype == kF32 ? 1 : 0; t < 3; ++t) {
-    const int columns = back ? kColumns[t] : kColumns[t] / 2;
+  if (!back && rows <= kFewRows) {
+    const int64_t turns = ((int64_t)depth + 8 * k.bk - 1) / (8 * k.bk);
+    const double groups = (double)((n + kFewColumns - 1) / kFewColumns) / kCUs;
+    least = 3.5 + turns * (groups > 1.0 ? groups : 1.0) *
+                      (ragged ? 2.6 + 0.07 * rows : 1.1 + 0.02 * rows);
+    best = {kFew, 1};
+  }
+  for (int t = 0; t < 3; ++t) {
+    const int columns = (t == kLarge ? k.columns : 128) / (back ? 1 : 2);
     const int64_t tiles = (rows + kRows[t] - 1) / kRows[t] * ((n + columns - 1) / columns);
-    const double slower = !ragged || dtype == kF32 ? 1.0 : t == kLarge ? 1.15 : 1.45;
+    const double slower = !ragged ? 1.0 : t == kLarge ? 1.15 : 1.45;
     for (int s = 1; s <= 32 && (s == 1 || 4 * s <= steps); s += s < 4 ? 1 : s / 2) {
-      const int64_t groups = tiles * s, full = groups / (kCUs * kPerCU[t]);
-      const int64_t rest = groups - full * kCUs * kPerCU[t], long_part = (steps + s - 1) / s;
-      const double* step = dtype == kF32 ? kStep32[t] : kStep16[t];
-      double us = full * (long_part * step[kPerCU[t] - 1] * slower + kRound[t]);
-      if (rest) {
-        const double one = t == kLarge && groups <= kCUs / 2 ? 1.15 : step[(rest + kCUs - 1) / kCUs - 1];
-        us += long_part * one * slower + kRound[t];
-      }
+      const int64_t at_once = kCUs * k.per_cu[t], groups = tiles * s, full = groups / at_once;
+      const int64_t rest = groups - full * at_once;
+      const double part = (double)((steps + s - 1) / s) * slower;
+      double us = full * (part * k.step[t][k.per_cu[t] - 1] + kRound[t]);
+      if (rest)
+        us += kRound[t] + part * (t == kLarge && groups <= kCUs / 2 ? k.few
+                                                                    : k.step[t][(rest - 1) / kCUs]);
       if (s > 1) us += 4.0 + 0.25 * s + 2.0 * 4.0 * s * (double)rows * n * (back ? 1 : 2) / 5e6;
       if (us < least) {
         least = us;
@@ -647,14 +828,19 @@ template <int DT, bool BACK, int ACT>
 hipError_t product(Product g, hipStream_t st) {
   const Shape s = shape_of(g.rows, g.n, g.depth, BACK, DT);
   g.splits = s.splits;
+  if constexpr (!BACK)
+    if (s.tile == kFew) {
+      const unsigned grid = (g.n + kFewColumns - 1) / kFewColumns;
+      k_gated_few<DT, ACT><<<grid, 64 * kFewWaves, 0, st>>>(g);
+      return hipGetLastError();
+    }
   hipError_t e = hipSuccess;
-  if (s.tile == kLarge) {
-    if constexpr (DT != kF32) e = product<DT, BACK, ACT, Large<DT, BACK>>(g, st);
-  } else if (s.tile == kSmall) {
+  if (s.tile == kLarge)
+    e = product<DT, BACK, ACT, Large<DT, BACK>>(g, st);
+  else if (s.tile == kSmall)
     e = product<DT, BACK, ACT, Small<DT, BACK>>(g, st);
-  } else {
+  else
     e = product<DT, BACK, ACT, Tiny<DT, BACK>>(g, st);
-  }
   if (e || g.splits == 1) return e;
   k_product_join<DT, BACK, ACT><<<blocks_for(g.rows * ((g.n + 7) / 8), 256), 256, 0, st>>>(g);
   return hipGetLastError();
