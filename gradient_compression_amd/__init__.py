@@ -806,8 +806,16 @@ def _activation(name):
     return code
 
 
+def _plain(t, dtype, dev):
+    """Whether t is a contiguous matrix of the type on the device: the common case, told in a few steps."""
+    return (isinstance(t, _types[1]) and t.get_device() == dev and t.dtype is dtype
+            and t.dim() == 2 and t.is_contiguous())
+
+
 def _weight(t, name, like, like_name, n, cols, dev):
     """(pointer, row pitch) of a weight of n x cols, of the type of another matrix."""
+    if _plain(t, like.dtype, dev) and t.size(0) == n and t.size(1) == cols:
+        return t.data_ptr(), cols
     p, ld, rows, width, _ = _matrix(t, name, dev)
     if t.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
@@ -816,11 +824,14 @@ def _weight(t, name, like, like_name, n, cols, dev):
     return p, ld
 
 
-def _rows_like(t, name, dev, like, like_name, cols):
-    """(pointer, row pitch) of a matrix with the leading dimensions and the type of another, and
-    `cols` columns; NULL for None."""
+def _rows_like(t, name, dev, like, like_name, rows, cols):
+    """(pointer, row pitch) of a matrix with the leading dimensions (`rows` in all) and the type of
+    another, and `cols` columns; NULL for None."""
     if t is None:
         return None, 0
+    if (_plain(t, like.dtype, dev) and like.dim() == 2 and t.size(0) == rows
+            and t.size(1) == cols):
+        return t.data_ptr(), cols
     p, ld, _, width, _ = _matrix(t, name, dev)
     if t.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype} like {like_name}, got {t.dtype}")
@@ -857,12 +868,12 @@ def gated_linear(x, w_gate, w_up, h, gate=None, up=None, activation: str = "silu
     up_, ld_u = _weight(w_up, "w_up", x, "x", n, cols, dev)
     if h is None:
         raise TypeError("h must be a torch tensor")
-    hp, ld_h = _rows_like(h, "h", dev, x, "x", n)
-    kg, ld_kg = _rows_like(gate, "gate", dev, x, "x", n)
-    ku, ld_ku = _rows_like(up, "up", dev, x, "x", n)
+    hp, ld_h = _rows_like(h, "h", dev, x, "x", rows, n)
+    kg, ld_kg = _rows_like(gate, "gate", dev, x, "x", rows, n)
+    ku, ld_ku = _rows_like(up, "up", dev, x, "x", rows, n)
     st = _raw_stream(stream, dev)
-    ws, ws_bytes, _keep = _workspace(workspace, gated_linear_workspace(rows, n, cols, x.dtype),
-                                     stream, dev)
+    need = gated_linear_workspace(rows, n, cols, x.dtype)
+    ws, ws_bytes, _keep = _workspace(workspace, need, stream, dev)
     _check(lib().gc_gated_linear(p, ld, code, rows, cols, gp, ld_g, up_, ld_u, n,
                                  _activation(activation), hp, ld_h, kg, ld_kg, ku, ld_ku, ws,
                                  ws_bytes, st), "gc_gated_linear")
@@ -902,7 +913,7 @@ def gated_linear_backward(dh, gate, up, dgate, dup, w_gate=None, w_up=None, dx=N
         if not isinstance(dx, _types[1]) or dx.dim() < 1:
             raise TypeError("dx must be a matrix")
         cols = dx.size(-1)
-        xp, ld_x = _rows_like(dx, "dx", dev, dh, "dh", cols)
+        xp, ld_x = _rows_like(dx, "dx", dev, dh, "dh", rows, cols)
         wg, ld_wg = _weight(w_gate, "w_gate", dh, "dh", n, cols, dev)
         wu, ld_wu = _weight(w_up, "w_up", dh, "dh", n, cols, dev)
         need = gated_linear_backward_workspace(rows, n, cols, dh.dtype)
@@ -979,7 +990,7 @@ def _grad_norm(arrays, norm, norms, workspace, stream, dev):
 
 def _grad_clip(arrays, tensors, max_norm, norm, out, factors, stream, dev):
     to, to_kinds, written = _outputs(out, arrays, tensors, dev)
-    f = 0 if factors is None else factors.numel()
+    f = factors.numel() if isinstance(factors, _types[1]) else 0
     _check(lib().gc_grad_clip(*arrays[3], len(arrays[1]), to.ctypes.data, to_kinds.ctypes.data,
                               float(max_norm), _scalar(norm, "norm", dev),
                               _array(factors, "factors", _types[0].float32, f, dev), f,

@@ -765,26 +765,31 @@ struct Shape {
 //              large          small       tiny
 //   16 bits    1.15 or 1.72   0.53 1.0    0.50 0.69 1.05
 //   fp32       1.6 or 2.4     1.4         0.84 1.47         (large: on up to half of the CUs, or all)
-// and a round of tiles 14, 7 or 4 us besides (launch, first loads, the results' way); a join 4 us, 0.25 us a
-// part and their bytes (written and read) at 5 TB/s.  Where the 16-bit types' rows are not whole 16 bytes
+// and a round of tiles 16, 7 or 4 us besides (launch, first loads, the results' way); a join 6 us (the host's
+// share among them), 0.5 us a part and their bytes (written and read) at 5 TB/s.  Where the 16-bit types' rows are not whole 16 bytes
 // wide, as where they start anywhere, a large step takes 1.15 times and the others 1.45 times as long.
 // Measured against every other choice over 50 drawn sizes, the rule's takes 5 % longer than the best.
 //
-// Up to 32 rows of a forward pass may go without tiles: 3.5 us, and 1.1 us (ragged 16-bit rows: 2.6) and a
-// little more with the rows for each 1 KB of a row's sum, with the workgroups in as many turns as fill the
-// CUs.  One row through 4096 x 4096 bf16 13.0 us (tiles 17.2), 3000 x 3001 19.4 (17.2), 1000 x 8000 19.2
-// (14.5); 32 rows through 4096 x 4096 16.9 (18.3), 11008 x 4096 44.4 (35.4).
+// Where one tile holds all rows nothing shares the weights' loads, which come from memory then: a tiny
+// tile's 16-bit step takes 0.78, 1.1 and 1.6 us, a small one's 0.75 and 1.3 (27 rows through 11008 x 4096 bf16,
+// the weights not in any cache: whole sums 53.8 us, in 4 parts 40.9).
+//
+// Up to 32 rows of a forward pass may go without tiles: 3.5 us, and for each 1 KB of a row's sum 1.65 us (fp32
+// 1.85, ragged 16-bit rows 2.9; less on part of the CUs) and a little more with the rows, with the
+// workgroups in as many turns as fill the CUs.  Weights not in any cache, one row through 4096 x 4096 bf16 16.0 us (tiles 21.2), 11008 x
+// 4096 44.7 (37.9), 8192 x 1000 11.0 (15.9); 32 rows through 4096 x 4096 27.4 (22.2).
 Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
   struct Costs {
     int columns, per_cu[3], bk;
     double few, step[3][3];
   };
   constexpr Costs k16 = {256, {1, 2, 3}, 64, 1.15, {{1.72}, {0.53, 1.0}, {0.50, 0.69, 1.05}}};
+  constexpr Costs k16far = {256, {1, 2, 3}, 64, 1.15, {{1.72}, {0.75, 1.3}, {0.78, 1.1, 1.6}}};
   constexpr Costs k32 = {128, {1, 1, 2}, 32, 1.6, {{2.4}, {1.4}, {0.84, 1.47}}};
   constexpr int kRows[3] = {256, 128, 64};
-  constexpr double kRound[3] = {14.0, 7.0, 4.0};
+  constexpr double kRound[3] = {16.0, 7.0, 4.0};
   constexpr int64_t kCUs = 256;
-  const Costs& k = dtype == kF32 ? k32 : k16;
+  const Costs& k = dtype == kF32 ? k32 : rows <= 128 ? k16far : k16;
   const int64_t steps = (back ? 2 : 1) * (((int64_t)depth + k.bk - 1) / k.bk);
   const bool ragged = dtype != kF32 && (depth % 8 || (back && n % 8));
   Shape best = {kTiny, 1};
@@ -792,8 +797,11 @@ Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
   if (!back && rows <= kFewRows) {
     const int64_t turns = ((int64_t)depth + 8 * k.bk - 1) / (8 * k.bk);
     const double groups = (double)((n + kFewColumns - 1) / kFewColumns) / kCUs;
-    least = 3.5 + turns * (groups > 1.0 ? groups : 1.0) *
-                      (ragged ? 2.6 + 0.07 * rows : 1.1 + 0.02 * rows);
+    const double some = groups < 1.0 ? groups : 1.0;
+    least = 3.5 + turns * (groups / some) *
+                      (dtype == kF32 ? 1.5 + 0.35 * some + 0.04 * rows
+                       : ragged      ? 2.0 + 0.9 * some + 0.075 * rows
+                                     : 1.0 + 0.65 * some + 0.055 * rows);
     best = {kFew, 1};
   }
   for (int t = 0; t < 3; ++t) {
@@ -808,7 +816,7 @@ Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
       if (rest)
         us += kRound[t] + part * (t == kLarge && groups <= kCUs / 2 ? k.few
                                                                     : k.step[t][(rest - 1) / kCUs]);
-      if (s > 1) us += 4.0 + 0.25 * s + 2.0 * 4.0 * s * (double)rows * n * (back ? 1 : 2) / 5e6;
+      if (s > 1) us += 6.0 + 0.5 * s + 2.0 * 4.0 * s * (double)rows * n * (back ? 1 : 2) / 5e6;
       if (us < least) {
         least = us;
         best = {(TileKind)t, s};
