@@ -795,7 +795,9 @@ Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
   Shape best = {kTiny, 1};
   double least = 1e300;
   if (!back && rows <= kFewRows) {
-    const int64_t turns = ((int64_t)depth + 8 * k.bk - 1) / (8 * k.bk);
+    // a turn: 1 KB of each row for the 8 waves; of less, most have nothing to do
+    const double turns = depth > 8 * k.bk ? (double)((depth - 1) / (8 * k.bk) + 1)
+                         : depth > 2 * k.bk ? depth / (8.0 * k.bk) : 0.3;
     const double groups = (double)((n + kFewColumns - 1) / kFewColumns) / kCUs;
     const double some = groups < 1.0 ? groups : 1.0;
     least = 3.5 + turns * (groups / some) *
