@@ -139,12 +139,13 @@ constexpr int kChunk = 16, kRowBytes = 128, kRowChunks = kRowBytes / kChunk;
 
 // A workgroup's tile, BM rows by BN columns (forward: BN / 2 of each projection), shared by WM x WN
 // waves.  A step sums 128 bytes of a row.  PARTS (1, or 3 of fp32): the bf16 values whose sum an element is
-// in LDS.
-template <int DT, bool BACK, int BM, int BN, int WM, int WN, int PARTS = 1>
+// in LDS.  AHEAD: steps from a piece's load to its way into LDS.
+template <int DT, bool BACK, int BM, int BN, int WM, int WN, int PARTS = 1, int AHEAD = 1>
 struct Tile {
   typedef typename Elt<DT>::T T;
   typedef Tile<DT, BACK, BM, BN, WM, WN> Whole;   // without parts
-  static constexpr int kParts = PARTS;
+  static constexpr int kParts = PARTS, kAhead = AHEAD;
+  static_assert(AHEAD == 1 || AHEAD == 2, "sets of pieces on their way");
   static constexpr int kBM = BM, kBN = BN, kWM = WM, kWN = WN;
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int kFM = BM / WM / 32, kFN = BN / WN / 32;
@@ -402,23 +403,22 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
     pb[1] += next_b;
     left -= C::kBK;
   };
-  u4 reg[kItems];
   // Item p of the next step, A's first: of a step that is whole (all of its pieces are there), and of
   // any: what lies behind the sum's end is 0.
   auto load_whole = [&](int p) {
     const char* q = p < C::kItemsA ? pa + off_a[p] : base_b(p - C::kItemsA) + off_b[p - C::kItemsA];
-    reg[p] = *reinterpret_cast<const u4_at_any*>(q);
+    return u4(*reinterpret_cast<const u4_at_any*>(q));
   };
   auto load_edge = [&](int p) {
     if (p < C::kItemsA) {
       const char* q = pa + row_a(p) * g.a[seg].ld * kSize;
-      reg[p] = load_piece(reinterpret_cast<const T*>(q), ca * E, left);
+      return load_piece(reinterpret_cast<const T*>(q), ca * E, left);
     } else {
       const int b = p - C::kItemsA;
       const int64_t row = BACK ? min(row_b(b), (int64_t)left - 1) : row_b(b);
       const char* q = base_b(b) + row * g.b[weight(b)].ld * kSize;
-      reg[p] = load_piece(reinterpret_cast<const T*>(q), cb * E, BACK ? g.n - n0 : left);
-      if (BACK && row_b(b) >= left) reg[p] = u4{};
+      const u4 w = load_piece(reinterpret_cast<const T*>(q), cb * E, BACK ? g.n - n0 : left);
+      return BACK && row_b(b) >= left ? u4{} : w;
     }
   };
   auto store = [&](char* stage, int p, const u4& w) {
@@ -485,11 +485,11 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
   };
 
   // The next step, whichever it is.
-  auto load_step = [&] {
+  auto load_step = [&](u4 (&to)[kItems]) {
     if (BACK && left <= 0 && seg == 0) start(1, 0);
 #pragma unroll
     for (int p = 0; p < kItems; ++p) {
-      load_edge(p);
+      to[p] = load_edge(p);
       __builtin_amdgcn_sched_barrier(0);   // one after the other: few registers
     }
     advance();
@@ -500,38 +500,46 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
 #pragma unroll
     for (int j = 0; j < C::kFN; ++j) acc[i][j] = f16v{};
   char *cur = s_mem, *nxt = s_mem + C::kStage;
+  constexpr int R = C::kAhead;
+  u4 reg[R][kItems];     // the pieces of the steps after the next: reg[0] is the first to be stored
   u4 fa[P][C::kFM], fb[P][C::kFN];
   if (steps > 0) {
     start(first >= steps_seg, first >= steps_seg ? first - steps_seg : first);
-    if (steps > 1 && whole_steps() > 1) {   // both steps' loads on their way at once
-      u4 ahead[kItems];
+    u4 now[kItems];
+    if (steps > R && whole_steps() > R) {   // all on their way at once
 #pragma unroll
-      for (int p = 0; p < kItems; ++p) load_whole(p);
-      advance();
+      for (int i = 0; i <= R; ++i) {
 #pragma unroll
-      for (int p = 0; p < kItems; ++p) {
-        ahead[p] = reg[p];
-        load_whole(p);
+        for (int p = 0; p < kItems; ++p) (i ? reg[i - 1] : now)[p] = load_whole(p);
+        advance();
       }
-      advance();
-#pragma unroll
-      for (int p = 0; p < kItems; ++p) store(cur, p, ahead[p]);
     } else {
-      load_step();
+      load_step(now);
 #pragma unroll
-      for (int p = 0; p < kItems; ++p) store(cur, p, reg[p]);
-      if (steps > 1) load_step();
+      for (int i = 0; i < R; ++i)
+        if (i + 1 < steps) load_step(reg[i]);
     }
+#pragma unroll
+    for (int p = 0; p < kItems; ++p) store(cur, p, now[p]);
     __syncthreads();
     read_b(cur, 0, fb);
     read_a(cur, 0, fa);
   }
   // One step: each slice is multiplied while the operands of the next are read.  During all slices but the
-  // last the next step's pieces, loaded a step ago, go to the other stage, each followed by the load of
-  // the piece of the step after, where that is whole.  Before the last slice all waves meet: the other
+  // last the next step's pieces, loaded kAhead steps ago, go to the other stage, each followed by the load
+  // of a piece of the step kAhead after it, where that is whole.  Before the last slice all waves meet: the other
   // stage is complete then, and nobody reads this one any more.
   int step = 0;
-  auto multiply_step = [&](auto load) {
+  auto turn = [&] {      // the set that was stored last is loaded last
+#pragma unroll
+    for (int p = 0; p < kItems; ++p)
+      if (R == 2) {
+        const u4 w = reg[0][p];
+        reg[0][p] = reg[R - 1][p];
+        reg[R - 1][p] = w;
+      }
+  };
+  auto multiply_step = [&](auto load, auto which) {
 #pragma unroll
     for (int s = 0; s < kSlices; ++s) {
       u4 na[P][C::kFM], nb[P][C::kFN];
@@ -541,8 +549,8 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
 #pragma unroll
       for (int p = 0; p < kItems; ++p)
         if (p * (kSlices - 1) / kItems == s) {
-          store(nxt, p, reg[p]);
-          if (load) load_whole(p);
+          store(nxt, p, reg[which][p]);
+          if (load) reg[which][p] = load_whole(p);
         }
       // all pairs of parts but those below 2^-23 of the product, the smallest first
 #pragma unroll
@@ -579,11 +587,20 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
   };
   while (step < steps) {
     if (BACK && left <= 0 && seg == 0) start(1, 0);
-    for (int n = min(whole_steps(), steps - 2 - step); n > 0; --n)
-      multiply_step(std::true_type());
-    if (BACK && left <= 0 && seg == 0 && step + 2 < steps) continue;
-    multiply_step(std::false_type());
-    if (step + 1 < steps) load_step();   // the step after the next: step is one further now
+    int n = min(whole_steps(), steps - 1 - R - step);
+    if constexpr (R == 2)
+      for (; n > 1; n -= 2) {   // the two sets in turn
+        multiply_step(std::true_type(), std::integral_constant<int, 0>());
+        multiply_step(std::true_type(), std::integral_constant<int, 1>());
+      }
+    for (; n > 0; --n) {
+      multiply_step(std::true_type(), std::integral_constant<int, 0>());
+      turn();
+    }
+    if (BACK && left <= 0 && seg == 0 && step + 1 + R < steps) continue;
+    multiply_step(std::false_type(), std::integral_constant<int, 0>());
+    if (step + R < steps) load_step(reg[0]);   // step is one further now
+    turn();
   }
 }
 
@@ -747,14 +764,14 @@ using Large = std::conditional_t<DT == kF32, Tile<DT, BACK, 256, 128, 4, 2, 3>,
                                  Tile<DT, BACK, 256, 256, 2, 4>>;
 template <int DT, bool BACK>
 using Small = Tile<DT, BACK, 128, 128, 2, 2, DT == kF32 ? 3 : 1>;
-template <int DT, bool BACK>
-using Tiny = Tile<DT, BACK, 64, 128, 2, 2, DT == kF32 ? 3 : 1>;
+template <int DT, bool BACK, int AHEAD = 1>
+using Tiny = Tile<DT, BACK, 64, 128, 2, 2, DT == kF32 ? 3 : 1, AHEAD>;
 
 enum TileKind { kLarge, kSmall, kTiny, kFew };   // kFew: the forward pass of few rows
 
 struct Shape {
   TileKind tile;
-  int splits;
+  int splits, ahead;   // ahead: of tiny 16-bit tiles
 };
 
 // A large tile needs the fewest loads a product, but leaves CUs idle where the result is small; a long sum
@@ -763,16 +780,21 @@ struct Shape {
 // takes, with 1, 2 and 3 workgroups on its CU, in microseconds (measured; a CU holds 1 large tile, of the
 // 16-bit types 2 small or 3 tiny ones, of fp32 1 and 2):
 //              large          small       tiny
-//   16 bits    1.15 or 1.72   0.53 1.0    0.50 0.69 1.05
+//   16 bits    1.15 or 1.72   0.53 1.0    0.43 0.69 1.05
 //   fp32       1.6 or 2.4     1.4         0.84 1.47         (large: on up to half of the CUs, or all)
-// and a round of tiles 16, 7 or 4 us besides (launch, first loads, the results' way); a join 6 us (the host's
+// and a round of tiles 16, 7 or 4 us (fp32 9, 7, 5) besides (launch, first loads, the results' way); a join 6 us (the host's
 // share among them), 0.5 us a part and their bytes (written and read) at 5 TB/s.  Where the 16-bit types' rows are not whole 16 bytes
 // wide, as where they start anywhere, a large step takes 1.15 times and the others 1.45 times as long.
-// Measured against every other choice over 50 drawn sizes, the rule's takes 5 % longer than the best.
+// Measured against every other choice over 80 drawn sizes, the rule's takes 3 % longer than the best.
+//
+// Up to 2 tiny 16-bit tiles a CU load their pieces two steps ahead, which the third workgroup's registers
+// would pay for: at 1 a CU the step waits for its loads (0.50 us one step ahead; with the weights from memory
+// 0.75 against 0.5: 27 rows through 4096 x 4096 bf16 47 and 33 us), at 3 others fill the time.  Sums of fewer
+// than 8 steps gain nothing and begin later (123 rows through 6963 x 158 8.2 and 10.9 us).
 //
 // Where one tile holds all rows nothing shares the weights' loads, which come from memory then: a tiny
-// tile's 16-bit step takes 0.78, 1.1 and 1.6 us, a small one's 0.75 and 1.3 (27 rows through 11008 x 4096 bf16,
-// the weights not in any cache: whole sums 53.8 us, in 4 parts 40.9).
+// tile's 16-bit step takes 0.5, 1.0 and 1.6 us, a small one's 0.75 and 1.3 (27 rows through 11008 x 4096 bf16,
+// the weights not in any cache: whole sums 44.7 us, in 4 parts 41.5).
 //
 // Up to 32 rows of a forward pass may go without tiles: 3.5 us, and for each 1 KB of a row's sum 1.65 us (fp32
 // 1.85, ragged 16-bit rows 2.9; less on part of the CUs) and a little more with the rows, with the
@@ -781,18 +803,19 @@ struct Shape {
 Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
   struct Costs {
     int columns, per_cu[3], bk;
-    double few, step[3][3];
+    double few, round[3], step[3][3];
   };
-  constexpr Costs k16 = {256, {1, 2, 3}, 64, 1.15, {{1.72}, {0.53, 1.0}, {0.50, 0.69, 1.05}}};
-  constexpr Costs k16far = {256, {1, 2, 3}, 64, 1.15, {{1.72}, {0.75, 1.3}, {0.78, 1.1, 1.6}}};
-  constexpr Costs k32 = {128, {1, 1, 2}, 32, 1.6, {{2.4}, {1.4}, {0.84, 1.47}}};
+  constexpr Costs k16 = {
+      256, {1, 2, 3}, 64, 1.15, {16.0, 7.0, 4.0}, {{1.72}, {0.53, 1.0}, {0.43, 0.69, 1.05}}};
+  constexpr Costs k16far = {
+      256, {1, 2, 3}, 64, 1.15, {16.0, 7.0, 4.0}, {{1.72}, {0.75, 1.3}, {0.5, 1.0, 1.6}}};
+  constexpr Costs k32 = {128, {1, 1, 2}, 32, 1.6, {9.0, 7.0, 5.0}, {{2.4}, {1.4}, {0.84, 1.47}}};
   constexpr int kRows[3] = {256, 128, 64};
-  constexpr double kRound[3] = {16.0, 7.0, 4.0};
   constexpr int64_t kCUs = 256;
   const Costs& k = dtype == kF32 ? k32 : rows <= 128 ? k16far : k16;
   const int64_t steps = (back ? 2 : 1) * (((int64_t)depth + k.bk - 1) / k.bk);
   const bool ragged = dtype != kF32 && (depth % 8 || (back && n % 8));
-  Shape best = {kTiny, 1};
+  Shape best = {kTiny, 1, 1};
   double least = 1e300;
   if (!back && rows <= kFewRows) {
     // a turn: 1 KB of each row for the 8 waves; of less, most have nothing to do
@@ -804,7 +827,7 @@ Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
                       (dtype == kF32 ? 1.5 + 0.35 * some + 0.04 * rows
                        : ragged      ? 2.0 + 0.9 * some + 0.075 * rows
                                      : 1.0 + 0.65 * some + 0.055 * rows);
-    best = {kFew, 1};
+    best = {kFew, 1, 1};
   }
   for (int t = 0; t < 3; ++t) {
     const int columns = (t == kLarge ? k.columns : 128) / (back ? 1 : 2);
@@ -814,14 +837,14 @@ Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
       const int64_t at_once = kCUs * k.per_cu[t], groups = tiles * s, full = groups / at_once;
       const int64_t rest = groups - full * at_once;
       const double part = (double)((steps + s - 1) / s) * slower;
-      double us = full * (part * k.step[t][k.per_cu[t] - 1] + kRound[t]);
+      double us = full * (part * k.step[t][k.per_cu[t] - 1] + k.round[t]);
       if (rest)
-        us += kRound[t] + part * (t == kLarge && groups <= kCUs / 2 ? k.few
+        us += k.round[t] + part * (t == kLarge && groups <= kCUs / 2 ? k.few
                                                                     : k.step[t][(rest - 1) / kCUs]);
       if (s > 1) us += 6.0 + 0.5 * s + 2.0 * 4.0 * s * (double)rows * n * (back ? 1 : 2) / 5e6;
       if (us < least) {
         least = us;
-        best = {(TileKind)t, s};
+        best = {(TileKind)t, s, t == kTiny && dtype != kF32 && groups <= 2 * kCUs && steps >= 8 * s ? 2 : 1};
       }
     }
   }
@@ -849,6 +872,8 @@ hipError_t product(Product g, hipStream_t st) {
     e = product<DT, BACK, ACT, Large<DT, BACK>>(g, st);
   else if (s.tile == kSmall)
     e = product<DT, BACK, ACT, Small<DT, BACK>>(g, st);
+  else if (s.ahead == 2)
+    e = product<DT, BACK, ACT, Tiny<DT, BACK, DT == kF32 ? 1 : 2>>(g, st);
   else
     e = product<DT, BACK, ACT, Tiny<DT, BACK>>(g, st);
   if (e || g.splits == 1) return e;
