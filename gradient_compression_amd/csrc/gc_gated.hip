@@ -6,10 +6,18 @@
 //              five matrices; then dX = dG Wg + dU Wu, one product whose sum runs over the columns of
 //              dG and then over those of dU.
 //
-// The products run on the matrix cores (32x32x16 for the 16-bit types, 32x32x2 fp32) with sums in
-// fp32.  Their first operand is the weight, so that a lane ends up with 16 neighbouring columns of one
-// row of the result (the 32 columns of a product are handed out in that order) and stores them in
-// 16-byte pieces.
+// The products run on the matrix cores (32x32x16 of 16-bit values; fp32 as three bf16 parts, six products a
+// pair) with sums in fp32.  Their first operand is the weight, so that a lane ends up with 16 neighbouring
+// columns of one row of the result (the 32 columns of a product are handed out in that order).  Both operands
+// come through registers into two stages of LDS, at any alignment; the backward pass's weight, whose rows are
+// the summed dimension, is read across its rows by LDS's transposing reads.
+//
+// Measured, 8192 rows, 4096 x 11008 bf16: forward with gate and up kept 1.29 to 1.32 ms (1120 to 1150 TFLOP/s),
+// backward 1.31 ms in all (the stream 0.155, 5.8 TB/s; the product 1.15, 1285 TFLOP/s).  Library products of the
+// same sizes, without the activation and its matrices, take 1.22 and 1.09 ms.  The matrix cores are busy for 61
+// and 72 % of the cycles, LDS (no bank conflicts) for 39 % of the forward pass's, at a clock of 1.7 GHz; the
+// forward pass stays behind by its results (541 MB) and activations, for which its tiles stand still.
+// Loading into LDS directly, 16-byte aligned rows only, was tried first: forward 1.32 ms, backward 1.50.
 #include <type_traits>
 
 #include "gc_act_internal.h"
@@ -212,7 +220,7 @@ __device__ __forceinline__ u4 load_piece(const T* p, int k, int end) {
 }
 
 // The three bf16 values whose sum each of 4 fp32 is, each the nearest to what the ones before it leave (8 bits
-// of 24).  Inf and NaN, and what rounds to Inf, leave NaN.
+// of 24).  Inf and NaN, and what rounds to Inf, leave NaN among them.
 __device__ __forceinline__ void parts_of(const u4& w, u2 (&part)[3]) {
   typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
   typedef float f2 __attribute__((ext_vector_type(2)));
@@ -619,9 +627,9 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
   f16v acc[C::kFM][C::kFN];
   sum_tile<DT, BACK, C>(g, s_mem, m0, n0, first, steps, acc);
   if constexpr (C::kParts > 1) {
-    // Parts do not multiply Inf (and what rounds to it) as it is: where NaN came out, the sum of whole
-    // elements says what it is.
-    bool nan = false;
+    // Parts do not multiply Inf as it is, and the first of them may overflow where the value does not: what
+    // came out as Inf or NaN is what the sum of whole elements says.
+    bool again = false;
     auto each = [&](auto&& f) {
 #pragma unroll
       for (int i = 0; i < C::kFM; ++i)
@@ -630,12 +638,13 @@ __global__ __launch_bounds__(C::kThreads, 2) void k_product(Product g) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) f(i, j, r);
     };
-    each([&](int i, int j, int r) { nan |= acc[i][j][r] != acc[i][j][r]; });
-    if (__syncthreads_or(nan)) {
+    auto finite = [](float v) { return fabsf(v) <= 3.402823466e38f; };   // NaN is not
+    each([&](int i, int j, int r) { again |= !finite(acc[i][j][r]); });
+    if (__syncthreads_or(again)) {
       f16v whole[C::kFM][C::kFN];
       sum_tile<DT, BACK, typename C::Whole>(g, s_mem, m0, n0, first, steps, whole);
       each([&](int i, int j, int r) {
-        if (acc[i][j][r] != acc[i][j][r]) acc[i][j][r] = whole[i][j][r];
+        if (!finite(acc[i][j][r])) acc[i][j][r] = whole[i][j][r];
       });
     }
   }
@@ -782,10 +791,11 @@ struct Shape {
 //              large          small       tiny
 //   16 bits    1.15 or 1.72   0.53 1.0    0.43 0.69 1.05
 //   fp32       1.6 or 2.4     1.4         0.84 1.47         (large: on up to half of the CUs, or all)
-// and a round of tiles 16, 7 or 4 us (fp32 9, 7, 5) besides (launch, first loads, the results' way); a join 6 us (the host's
-// share among them), 0.5 us a part and their bytes (written and read) at 5 TB/s.  Where the 16-bit types' rows are not whole 16 bytes
-// wide, as where they start anywhere, a large step takes 1.15 times and the others 1.45 times as long.
-// Measured against every other choice over 80 drawn sizes, the rule's takes 3 % longer than the best.
+// and a round of tiles 16, 7 or 4 us (fp32 9, 7, 5) besides (launch, first loads, the results' way); a join
+// 6 us (the host's share among them), 0.5 us a part and their bytes (written and read) at 5 TB/s.  Where
+// the 16-bit types' rows are not whole 16 bytes wide, as where they start anywhere, a large step takes 1.15
+// times and the others 1.45 times as long.  Measured against every other choice over 80 drawn sizes, the rule's
+// takes 3 % longer than the best.
 //
 // Up to 2 tiny 16-bit tiles a CU load their pieces two steps ahead, which the third workgroup's registers
 // would pay for: at 1 a CU the step waits for its loads (0.50 us one step ahead; with the weights from memory
@@ -798,8 +808,9 @@ struct Shape {
 //
 // Up to 32 rows of a forward pass may go without tiles: 3.5 us, and for each 1 KB of a row's sum 1.65 us (fp32
 // 1.85, ragged 16-bit rows 2.9; less on part of the CUs) and a little more with the rows, with the
-// workgroups in as many turns as fill the CUs.  Weights not in any cache, one row through 4096 x 4096 bf16 16.0 us (tiles 21.2), 11008 x
-// 4096 44.7 (37.9), 8192 x 1000 11.0 (15.9); 32 rows through 4096 x 4096 27.4 (22.2).
+// workgroups in as many turns as fill the CUs.  Weights not in any cache, one row through 4096 x 4096 bf16
+// 16.0 us (tiles 21.2), 11008 x 4096 44.7 (37.9), 8192 x 1000 11.0 (15.9); 32 rows through 4096 x 4096 27.4
+// (22.2).
 Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
   struct Costs {
     int columns, per_cu[3], bk;
@@ -817,7 +828,7 @@ Shape shape_of(int64_t rows, int32_t n, int32_t depth, bool back, int dtype) {
   const bool ragged = dtype != kF32 && (depth % 8 || (back && n % 8));
   Shape best = {kTiny, 1, 1};
   double least = 1e300;
-  if (!back && rows <= kFewRows) {
+  if (!back && rows <= kFewRows && n < 1 << 26) {   // a launch's threads are counted in 32 bits
     // a turn: 1 KB of each row for the 8 waves; of less, most have nothing to do
     const double turns = depth > 8 * k.bk ? (double)((depth - 1) / (8 * k.bk) + 1)
                          : depth > 2 * k.bk ? depth / (8.0 * k.bk) : 0.3;

@@ -4,7 +4,9 @@
  * The main path is error-feedback Top-k (below).  The same plan also serves threshold and
  * Random-k sparsification, 1-bit sign and QSGD codecs, local gradient clipping, and the
  * receiver-side sum of several workers' payloads; each entry point states its own
- * definition and source.
+ * definition and source.  Without a plan: 8-bit activation checkpoints with the norm and the weight
+ * gradient that use them, the gated feed-forward block between these, and the clipping of a whole
+ * model's gradients by their global norm on their way into the flat gradient.
  *
  * The operation, per segment (one parameter tensor) of a worker's flat fp32 gradient,
  * is the error-feedback Top-k step of "Communication Optimization > Gradient Compression"
@@ -496,8 +498,11 @@ int gc_act_weight_grad(const void* dy, int64_t ld_dy, int32_t dtype, int64_t row
  *   gate = round(G);  up = round(U)  (what the backward pass starts from; either may be NULL)
  * with act(g) = g / (1 + exp(-g)) (GC_ACT_SILU), g * Phi(g) with the normal distribution function Phi
  * (GC_ACT_GELU), or g / (1 + exp(-2 sqrt(2 / pi) (g + 0.044715 g^3))) (GC_ACT_GELU_TANH), in fp32.
- * Everything shares dtype.  Products of bf16 and fp16 are exact; as in gc_act_weight_grad, values,
- * products and sums below 2^-126 in magnitude may count as 0.  cols = 0 gives zeros.
+ * Everything shares dtype.  Products of bf16 and fp16 are exact.  An fp32 value is multiplied as the sum
+ * of three bf16 values (its 24 bits), the pairs below 2^-23 of a product left out, which its sum rounds
+ * away; Inf, NaN and what overflows come out as one fp32 sum has them.  As in gc_act_weight_grad, values
+ * (or the low bits of a value), products and sums below 2^-126 in magnitude may count as 0.  The order of a
+ * sum depends on the sizes and types alone.  cols = 0 gives zeros.
  * x is the y of a gc_rmsnorm; the weights' gradients are gc_act_weight_grad's of dgate and dup, with
  * that norm's checkpoint.
  *   workspace : 16-byte aligned, of at least gc_gated_linear_workspace bytes (may be NULL where that is
@@ -517,7 +522,8 @@ int gc_gated_linear(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, in
 /*
  * The block's backward pass from the kept gate and up:
  *   dgate = round(dh * up * act'(gate));  dup = round(dh * act(gate))  to dtype;
- *   dx = round(dgate w_gate + dup w_up) of dgate and dup as they are stored (fp32 sums).
+ *   dx = round(dgate w_gate + dup w_up) of dgate and dup as they are stored (fp32 sums, as above),
+ * with act' the derivative of act, each within a few units of fp32 of its terms.
  *   dgate, dup : may each be dh, gate or up itself (not both the same).
  *   dx         : may be NULL; then only dgate and dup are formed, and cols, the weights and the
  *                workspace are not looked at.

@@ -185,3 +185,31 @@ def test_what_lies_behind_the_last_row_stays():
             gca.gated_linear_backward(dh, v[1], v[2], v[3], v[4], w_gate=wg, w_up=wu, dx=v[5])
             for o in outs:
                 assert bool((o[:20] == 7.0).all()) and bool((o[20 + rows:] == 7.0).all())
+
+
+def test_fp32_products_just_below_the_largest_number():
+    """A value whose first bf16 part is a power of two above it: that part's product passes fp32's range where the
+    value's own, exact here, does not."""
+    rows, n, cols = 70, 100, 520
+    near = 2.0 ** 65 - 2.0 ** 55
+    x = torch.zeros(rows, cols, device="cuda")
+    wg, wu = torch.zeros(n, cols, device="cuda"), torch.zeros(n, cols, device="cuda")
+    x[3, 5], wg[:, 5], wu[:, 5] = near, 2.0 ** 63, 2.0 ** -100
+    h, gate, up = (torch.empty(rows, n, device="cuda") for _ in range(3))
+    gca.gated_linear(x, wg, wu, h, gate=gate, up=up)
+    want = torch.zeros(rows, n, dtype=torch.float64, device="cuda")
+    want[3] = near * 2.0 ** 63
+    assert torch.equal(gate.double(), want)
+    want[3] *= near * 2.0 ** -100      # silu is the identity there, to 16 * 2^-24 of it as everywhere
+    assert bool(((h.double() - want).abs() <= 17 * 2.0 ** -24 * want).all())
+    # dgate = 2^65 - 2^55 to a few units, as silu's slope at 100 is 1 to 16 * 2^-24; dup's weights are 0
+    dh = torch.zeros(rows, n, device="cuda")
+    dh[2, 4] = near
+    wg, wu = torch.zeros(n, cols, device="cuda"), torch.zeros(n, cols, device="cuda")
+    wg[4] = 2.0 ** 63
+    dx, dg, du = torch.empty(rows, cols, device="cuda"), torch.empty_like(dh), torch.empty_like(dh)
+    gca.gated_linear_backward(dh, torch.full_like(dh, 100.0), torch.ones_like(dh), dg, du, w_gate=wg,
+                              w_up=wu, dx=dx)
+    want = torch.zeros(rows, cols, dtype=torch.float64, device="cuda")
+    want[2] = near * 2.0 ** 63
+    assert bool(((dx.double() - want).abs() <= 20 * 2.0 ** -24 * want).all())
