@@ -12,8 +12,8 @@
 // come through registers into two stages of LDS, at any alignment; the backward pass's weight, whose rows are
 // the summed dimension, is read across its rows by LDS's transposing reads.
 //
-// Measured, 8192 rows, 4096 x 11008 bf16: forward with gate and up kept 1.29 to 1.32 ms (1120 to 1150 TFLOP/s),
-// backward 1.31 ms in all (the stream 0.155, 5.8 TB/s; the product 1.15, 1285 TFLOP/s).  Library products of the
+// Measured, 8192 rows, 4096 x 11008 bf16: forward with gate and up kept 1.19 to 1.24 ms (1190 to 1240 TFLOP/s),
+// backward 1.28 to 1.33 ms in all (the stream 0.155, 5.8 TB/s; the product 1.15).  Library products of the
 // same sizes, without the activation and its matrices, take 1.22 and 1.09 ms.  The matrix cores are busy for 61
 // and 72 % of the cycles, LDS (no bank conflicts) for 39 % of the forward pass's, at a clock of 1.7 GHz; the
 // forward pass stays behind by its results (541 MB) and activations, for which its tiles stand still.
@@ -360,20 +360,24 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
   const int wm = wave / C::kWN * (C::kFM * 32), wn = wave % C::kWN * (C::kFN * 32);
   const int steps_seg = (g.depth + C::kBK - 1) / C::kBK;
 
-  // This thread's piece of every item: A's row p * kRowsA + ra, piece ca of the step; B's likewise.
-  // Whole elements lie in the order of the threads, so that the piece is the one which belongs there; parts
-  // find their places when they are stored.
-  const int ra = threadIdx.x / kRowChunks, sa = threadIdx.x % kRowChunks;
-  const int rb = threadIdx.x / C::kPiecesB, sb = threadIdx.x % C::kPiecesB;
-  const int ca = P > 1 ? sa : sa ^ ((ra >> 1) & 7);
-  const int cb = P > 1  ? sb
-                 : BACK ? block_at<kWide>(rb, sb >> 2) * 4 + (sb & 3)
-                        : sb ^ ((rb >> 1) & 7);
+  // Thread t's piece of every item: A's row p * kRowsA + t / kRowChunks, piece piece_a(t) of the step; B's
+  // likewise.  Whole elements lie in the order of the threads, so that the piece is the one which belongs
+  // there; parts find their places when they are stored.
+  auto piece_a = [](int t) {
+    const int c = t % kRowChunks;
+    return P > 1 ? c : c ^ ((t / kRowChunks >> 1) & 7);
+  };
+  auto piece_b = [](int t) {
+    const int r = t / C::kPiecesB, c = t % C::kPiecesB;
+    return P > 1 ? c : BACK ? block_at<kWide>(r, c >> 2) * 4 + (c & 3) : c ^ ((r >> 1) & 7);
+  };
   // Where the rows of the items lie from the tile's first (rows past the last one read it; what they add
   // up is not stored).
-  auto row_a = [&](int p) { return min(m0 + p * C::kRowsA + ra, g.rows - 1) - m0; };
-  auto row_b = [&](int p) {
-    const int r = p * C::kRowsB + rb;
+  auto row_a = [&](int t, int p) {
+    return min(m0 + p * C::kRowsA + t / kRowChunks, g.rows - 1) - m0;
+  };
+  auto row_b = [&](int t, int p) {
+    const int r = p * C::kRowsB + t / C::kPiecesB;
     return (int64_t)(BACK ? r : min(n0 + (r >> 6) * 32 + column_of(r & 31), g.n - 1) - n0);
   };
   int seg = 0, left = 0;   // of the sum, from the next step on: the segment, what is left of it
@@ -398,11 +402,12 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
       pb[i] = static_cast<const char*>(b.p) + (BACK ? (int64_t)n0 : n0 * b.ld) * kSize + from * next_b;
     }
 #pragma unroll
-    for (int p = 0; p < C::kItemsA; ++p) off_a[p] = (uint32_t)(row_a(p) * a.ld * kSize) + ca * kChunk;
+    for (int p = 0; p < C::kItemsA; ++p)
+      off_a[p] = (uint32_t)(row_a(threadIdx.x, p) * a.ld * kSize) + piece_a(threadIdx.x) * kChunk;
 #pragma unroll
     for (int p = 0; p < C::kItemsB; ++p)
-      off_b[p] = (uint32_t)(row_b(p) * g.b[weight(p)].ld * kSize) +
-                 (BACK && n0 + cb * E >= g.n ? 0 : cb * kChunk);
+      off_b[p] = (uint32_t)(row_b(threadIdx.x, p) * g.b[weight(p)].ld * kSize) +
+                 (BACK && n0 + piece_b(threadIdx.x) * E >= g.n ? 0 : piece_b(threadIdx.x) * kChunk);
   };
   auto base_b = [&](int p) { return pb[BACK || C::kRowsB == 64 ? 0 : (p * C::kRowsB >> 5) & 1]; };
   auto advance = [&] {
@@ -418,21 +423,27 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
     return u4(*reinterpret_cast<const u4_at_any*>(q));
   };
   auto load_edge = [&](int p) {
+    // where this thread's pieces lie is found anew: kept through the steps before, it would take registers that
+    // the large tiles do not have (70 values of a thread went to memory and back, 0.2 GB in a call of 8192 rows)
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
     if (p < C::kItemsA) {
-      const char* q = pa + row_a(p) * g.a[seg].ld * kSize;
-      return load_piece(reinterpret_cast<const T*>(q), ca * E, left);
+      const char* q = pa + row_a(t, p) * g.a[seg].ld * kSize;
+      return load_piece(reinterpret_cast<const T*>(q), piece_a(t) * E, left);
     } else {
       const int b = p - C::kItemsA;
-      const int64_t row = BACK ? min(row_b(b), (int64_t)left - 1) : row_b(b);
+      const int64_t row = BACK ? min(row_b(t, b), (int64_t)left - 1) : row_b(t, b);
       const char* q = base_b(b) + row * g.b[weight(b)].ld * kSize;
-      const u4 w = load_piece(reinterpret_cast<const T*>(q), cb * E, BACK ? g.n - n0 : left);
-      return BACK && row_b(b) >= left ? u4{} : w;
+      const u4 w = load_piece(reinterpret_cast<const T*>(q), piece_b(t) * E, BACK ? g.n - n0 : left);
+      return BACK && row_b(t, b) >= left ? u4{} : w;
     }
   };
   auto store = [&](char* stage, int p, const u4& w) {
     if constexpr (P == 1) {
       *reinterpret_cast<u4*>(stage + (p * C::kThreads + threadIdx.x) * kChunk) = w;
     } else {
+      const int ra = threadIdx.x / kRowChunks, sa = threadIdx.x % kRowChunks;
+      const int rb = threadIdx.x / C::kPiecesB, sb = threadIdx.x % C::kPiecesB;
       u2 part[3];
       parts_of(w, part);
 #pragma unroll
@@ -440,12 +451,12 @@ __device__ __forceinline__ void sum_tile(const Product& g, char* s_mem, int64_t 
         const int b = p - C::kItemsA;
         char* to = stage;
         if (p < C::kItemsA)
-          to += piece_at<P>(p * C::kRowsA + ra, ca >> 1, q) + (ca & 1) * 8;
+          to += piece_at<P>(p * C::kRowsA + ra, sa >> 1, q) + (sa & 1) * 8;
         else if (!BACK)
-          to += C::kBytesA + piece_at<P>(b * C::kRowsB + rb, cb >> 1, q) + (cb & 1) * 8;
+          to += C::kBytesA + piece_at<P>(b * C::kRowsB + rb, sb >> 1, q) + (sb & 1) * 8;
         else
           to += C::kBytesA + (q * C::kBK + b * C::kRowsB + rb) * C::kPitchB +
-                block_at<false>(rb, cb >> 3) * 64 + (cb & 7) * 8;
+                block_at<false>(rb, sb >> 3) * 64 + (sb & 7) * 8;
         *reinterpret_cast<u2*>(to) = part[q];
       }
     }
