@@ -14,9 +14,9 @@
 //
 // Measured, 8192 rows, 4096 x 11008 bf16: forward with gate and up kept 1.19 to 1.24 ms (1190 to 1240 TFLOP/s),
 // backward 1.28 to 1.33 ms in all (the stream 0.155, 5.8 TB/s; the product 1.15).  Library products of the
-// same sizes, without the activation and its matrices, take 1.22 and 1.09 ms.  The matrix cores are busy for 61
-// and 72 % of the cycles, LDS (no bank conflicts) for 39 % of the forward pass's, at a clock of 1.7 GHz; the
-// forward pass stays behind by its results (541 MB) and activations, for which its tiles stand still.
+// same sizes, without the activation and its matrices, take 1.22 and 1.09 ms.  The matrix cores are busy for 70
+// and 77 % of the cycles, LDS (hardly a bank conflict) for 47 and 48 %, at a clock of 1.7 GHz; the forward pass
+// has its results (541 MB) and activations besides, for which its tiles stand still.
 // Loading into LDS directly, 16-byte aligned rows only, was tried first: forward 1.32 ms, backward 1.50.
 #include <type_traits>
 

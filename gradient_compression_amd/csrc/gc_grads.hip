@@ -3,6 +3,14 @@
 // Both are streams: the norm reads every tensor once, the scaling reads it again (part of it from the
 // 256 MB cache) and writes the result.  Squares and sums are in double, so that neither the range
 // of fp32 nor the length of the sum matters; the order of a sum depends on the tensors' sizes alone.
+// A block of 4 waves takes a run of 16384-element chunks, so that many small tensors load it as evenly as a
+// large one; it has 4 accesses of 16 bytes a lane in flight (8 gained nothing).
+//
+// Measured: 1.07e9 bf16 elements into one fp32 tensor 1605 us in all, of which the norm reads at 5.9 TB/s and the
+// scaling moves 5.2 TB/s (a plain copy 4.8); 335 M elements in 391 tensors 540 us; 335 M in place under
+// the limit, which nothing is written for, 238 us (5.65 TB/s).  161 tensors of 25 M elements take the GPU
+// 28 us, and the host 66 to 70 us to look at.  Going through the tensors from their end when scaling, where the
+// cache still holds the last ones, gained 1 % at most.
 #include <type_traits>
 
 #include "gc_grads.h"
@@ -164,7 +172,7 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
 }
 
 // 16 bytes of the wider type a lane, so that what a wave stores lies without gaps (bf16 to fp32 by 8
-// elements a lane, in two stores with gaps: 1409 us in place of 1286 for 2^30 elements).
+// elements a lane, in two stores with gaps: 1409 us in place of 1286 for 1.07e9 elements).
 template <int DI, int DO, bool STREAM>
 __device__ __forceinline__ void scale(const typename Elt<DI>::T* p, typename Elt<DO>::T* out, int n,
                                       float f) {
