@@ -82,20 +82,22 @@ __device__ __forceinline__ void activate(float g, float* act, float* slope) {
 }
 
 // v[r] = act(v[r]) * u[r].  The forward pass stands still for this, so that silu takes a short way where
-// no lane of the wave has |g| > 16: there exp(-g) needs no correction (its argument's rounding is at most
-// 16 * 2^-24 of it) and stays far from the ends of fp32's range.
+// |g| <= 16: there exp(-g) needs no correction (its argument's rounding is at most 16 * 2^-24 of it; act is
+// within 20 * 2^-24) and stays far from the ends of fp32's range.  Which way is taken goes by the value alone:
+// a wave in which some |g| > 16 goes both ways, and each value takes its own.  (8192 rows through 11008 x 4096
+// bf16: 1220 us where no wave does, 1264 where all do.)
 template <int ACT, int N>
 __device__ __forceinline__ void gate(float (&v)[N], const float (&u)[N]) {
+  auto near = [](float g) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269502f));
+  };
   if (ACT == kSilu) {
     float most = 0.0f;
 #pragma unroll
-    for (int r = 0; r < N; ++r) most = fmaxf(most, fabsf(v[r]));   // of numbers: NaN stays NaN below
+    for (int r = 0; r < N; ++r) most = fmaxf(most, fabsf(v[r]));   // of numbers: NaN stays NaN either way
     if (__ballot(most > 16.0f) == 0) {
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const float e = __builtin_amdgcn_exp2f(v[r] * -1.44269502f);
-        v[r] = v[r] * __builtin_amdgcn_rcpf(1.0f + e) * u[r];
-      }
+      for (int r = 0; r < N; ++r) v[r] = near(v[r]) * u[r];
       return;
     }
   }
@@ -103,6 +105,7 @@ __device__ __forceinline__ void gate(float (&v)[N], const float (&u)[N]) {
   for (int r = 0; r < N; ++r) {
     float act, slope;
     activate<ACT>(v[r], &act, &slope);
+    if (ACT == kSilu) act = fabsf(v[r]) > 16.0f ? act : near(v[r]);
     v[r] = act * u[r];
   }
 }

@@ -502,7 +502,8 @@ int gc_act_weight_grad(const void* dy, int64_t ld_dy, int32_t dtype, int64_t row
  * of three bf16 values (its 24 bits), the pairs below 2^-23 of a product left out, which its sum rounds
  * away; Inf, NaN and what overflows come out as one fp32 sum has them.  As in gc_act_weight_grad, values
  * (or the low bits of a value), products and sums below 2^-126 in magnitude may count as 0.  The order of a
- * sum depends on the sizes and types alone.  cols = 0 gives zeros.
+ * sum depends on the sizes and types alone, and a result's bits on its row of x and its two rows of the
+ * weights besides: what stands in other rows does not reach it.  cols = 0 gives zeros.
  * x is the y of a gc_rmsnorm; the weights' gradients are gc_act_weight_grad's of dgate and dup, with
  * that norm's checkpoint.
  *   workspace : 16-byte aligned, of at least gc_gated_linear_workspace bytes (may be NULL where that is
