@@ -32,9 +32,10 @@ int check_sizes(const int64_t* sizes, int32_t n) {
   for (int32_t t = 0; t < n; ++t) {
     if (sizes[t] < 0) return GC_ERR_INVALID_ARG;
     if (sizes[t] > kMostElements) return GC_ERR_UNSUPPORTED;
-    total += sizes[t];   // at most 2^20 * 2^44
+    total += sizes[t];   // at most twice kMostElements
+    if (total > kMostElements) return GC_ERR_UNSUPPORTED;
   }
-  return total > kMostElements ? GC_ERR_UNSUPPORTED : GC_OK;
+  return GC_OK;
 }
 
 bool valid_tensors(const void* const* p, const int64_t* sizes, const int32_t* dtypes, int32_t n) {
