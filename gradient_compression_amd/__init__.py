@@ -979,12 +979,12 @@ def _scalar(t, name, dev):
 def _grad_norm(arrays, norm, norms, workspace, stream, dev):
     at = arrays[3]
     n, L = len(arrays[1]), lib()
+    st = _raw_stream(stream, dev)
+    to, each = _scalar(norm, "norm", dev), _array(norms, "norms", _types[0].float32, n, dev)
     need = ctypes.c_int64()
     _check(L.gc_grad_norm_workspace(at[1], n, ctypes.byref(need)), "gc_grad_norm_workspace")
     ws, ws_bytes, _keep = _workspace(workspace, need.value, stream, dev)
-    _check(L.gc_grad_norm(*at, n, _scalar(norm, "norm", dev),
-                          _array(norms, "norms", _types[0].float32, n, dev), ws, ws_bytes,
-                          _raw_stream(stream, dev)), "gc_grad_norm")
+    _check(L.gc_grad_norm(*at, n, to, each, ws, ws_bytes, st), "gc_grad_norm")
     _types[4]((norm,) if norms is None else (norm, norms))
 
 
