@@ -45,7 +45,8 @@ EXPORTS = ("gc_plan_create", "gc_plan_destroy", "gc_plan_total_k", "gc_plan_layo
            "gc_rmsnorm_backward_workspace", "gc_rmsnorm_backward",
            "gc_act_weight_grad_workspace", "gc_act_weight_grad",
            "gc_gated_linear_workspace", "gc_gated_linear", "gc_gated_linear_backward_workspace",
-           "gc_gated_linear_backward", "gc_grad_norm_workspace", "gc_grad_norm", "gc_grad_clip")
+           "gc_gated_linear_backward", "gc_grad_norm_workspace", "gc_grad_norm", "gc_grad_clip",
+           "gc_clip_grad_norm")
 
 _libs: dict = {}
 
@@ -125,6 +126,7 @@ def lib(variant: str | None = None) -> ctypes.CDLL:
         "gc_grad_norm_workspace": [vp, i32, vp],
         "gc_grad_norm": [vp, vp, vp, i32, vp, vp, vp, i64, vp],
         "gc_grad_clip": [vp, vp, vp, i32, vp, vp, f32, vp, vp, i64, vp],
+        "gc_clip_grad_norm": [vp, vp, vp, i32, vp, vp, f32, vp, vp, vp, i64, vp, i64, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -934,9 +936,9 @@ def _tensors(ts, name, dev):
     three."""
     Tensor, codes = _types[1], _types[2]
     try:      # the shortest ways: a model has hundreds of them
-        ptrs = np.array(list(map(Tensor.data_ptr, ts)), np.uint64)
-        sizes = np.array(list(map(Tensor.numel, ts)), np.int64)
-        kinds = np.array([codes[t.dtype] for t in ts], np.int32)
+        ptrs = np.fromiter(map(Tensor.data_ptr, ts), np.uint64, len(ts))
+        sizes = np.fromiter(map(Tensor.numel, ts), np.int64, len(ts))
+        kinds = np.fromiter([codes[t.dtype] for t in ts], np.int32, len(ts))
         fine = all(map(Tensor.is_contiguous, ts)) and set(map(Tensor.get_device, ts)) <= {dev}
     except (AttributeError, KeyError, RuntimeError, TypeError):
         fine = False
@@ -959,12 +961,10 @@ def _outputs(out, arrays, tensors, dev):
     if out is None:
         return ptrs, kinds, tensors
     if isinstance(out, _types[1]):
-        total = int(sizes.sum())
-        at, code = _columns(out, "out", total, dev)
-        step = out.element_size()
-        first = np.concatenate(([0], np.cumsum(sizes)[:-1])) if len(sizes) else sizes
-        return ((first * step).astype(np.uint64) + np.uint64(at or 0),
-                np.full(len(sizes), code, np.int32), (out,))
+        ends = sizes.cumsum()
+        at, code = _columns(out, "out", int(ends[-1]) if len(ends) else 0, dev)
+        first = (ends - sizes) * out.element_size()
+        return first + (at or 0), np.full(len(sizes), code, np.int32), (out,)
     out = list(out)
     got = _tensors(out, "out", dev)
     if not np.array_equal(got[1], sizes):
@@ -976,26 +976,22 @@ def _scalar(t, name, dev):
     return _array(t, name, _types[0].float32, 1, dev)
 
 
-def _grad_norm(arrays, norm, norms, workspace, stream, dev):
-    at = arrays[3]
-    n, L = len(arrays[1]), lib()
-    st = _raw_stream(stream, dev)
-    to, each = _scalar(norm, "norm", dev), _array(norms, "norms", _types[0].float32, n, dev)
+def _norm_outputs(arrays, norm, norms, dev):
+    """Pointers of what the norm writes."""
+    return _scalar(norm, "norm", dev), _array(norms, "norms", _types[0].float32, len(arrays[1]), dev)
+
+
+def _norm_workspace(arrays, workspace, stream, dev):
     need = ctypes.c_int64()
-    _check(L.gc_grad_norm_workspace(at[1], n, ctypes.byref(need)), "gc_grad_norm_workspace")
-    ws, ws_bytes, _keep = _workspace(workspace, need.value, stream, dev)
-    _check(L.gc_grad_norm(*at, n, to, each, ws, ws_bytes, st), "gc_grad_norm")
-    _types[4]((norm,) if norms is None else (norm, norms))
+    _check(lib().gc_grad_norm_workspace(arrays[3][1], len(arrays[1]), ctypes.byref(need)),
+           "gc_grad_norm_workspace")
+    return _workspace(workspace, need.value, stream, dev)
 
 
-def _grad_clip(arrays, tensors, max_norm, norm, out, factors, stream, dev):
-    to, to_kinds, written = _outputs(out, arrays, tensors, dev)
-    f = factors.numel() if isinstance(factors, _types[1]) else 0
-    _check(lib().gc_grad_clip(*arrays[3], len(arrays[1]), to.ctypes.data, to_kinds.ctypes.data,
-                              float(max_norm), _scalar(norm, "norm", dev),
-                              _array(factors, "factors", _types[0].float32, f, dev), f,
-                              _raw_stream(stream, dev)), "gc_grad_clip")
-    _types[4](list(written) if factors is None else [*written, factors])
+def _factors(factors, dev):
+    """(pointer, elements) of the factors; NULL for None."""
+    n = factors.numel() if isinstance(factors, _types[1]) else 0
+    return _array(factors, "factors", _types[0].float32, n, dev), n
 
 
 def grad_norm_workspace(sizes) -> int:
@@ -1014,8 +1010,12 @@ def grad_norm(tensors, norm, norms=None, workspace=None, stream=None):
     each one's.  ``workspace``: a tensor of grad_norm_workspace bytes; allocated for the call when
     None."""
     dev = _device_of(norm, "norm")
-    tensors = list(tensors)
-    _grad_norm(_tensors(tensors, "tensors", dev), norm, norms, workspace, stream, dev)
+    tensors = list(tensors)      # held until the launch
+    arrays = _tensors(tensors, "tensors", dev)
+    st, to = _raw_stream(stream, dev), _norm_outputs(arrays, norm, norms, dev)
+    ws, ws_bytes, _keep = _norm_workspace(arrays, workspace, stream, dev)
+    _check(lib().gc_grad_norm(*arrays[3], len(arrays[1]), *to, ws, ws_bytes, st), "gc_grad_norm")
+    _types[4]((norm,) if norms is None else (norm, norms))
 
 
 def grad_clip(tensors, max_norm: float, norm, out=None, factors=None, stream=None):
@@ -1026,18 +1026,29 @@ def grad_clip(tensors, max_norm: float, norm, out=None, factors=None, stream=Non
     (float32): all set to f, for Plan.set_gradient_scale."""
     dev = _device_of(norm, "norm")
     tensors = list(tensors)
-    _grad_clip(_tensors(tensors, "tensors", dev), tensors, max_norm, norm, out, factors, stream, dev)
+    arrays = _tensors(tensors, "tensors", dev)
+    to, to_kinds, written = _outputs(out, arrays, tensors, dev)
+    _check(lib().gc_grad_clip(*arrays[3], len(arrays[1]), to.ctypes.data, to_kinds.ctypes.data,
+                              float(max_norm), _scalar(norm, "norm", dev), *_factors(factors, dev),
+                              _raw_stream(stream, dev)), "gc_grad_clip")
+    _types[4](list(written) if factors is None else [*written, factors])
 
 
 def clip_grad_norm(tensors, max_norm: float, norm, out=None, norms=None, factors=None,
                    workspace=None, stream=None):
     """grad_norm, and grad_clip by it: the gradients of a whole model scaled so that their norm is at
-    most max_norm, in place or into ``out``."""
+    most max_norm, in place or into ``out``.  A refused call leaves norm and norms as they were, too."""
     dev = _device_of(norm, "norm")
     tensors = list(tensors)
     arrays = _tensors(tensors, "tensors", dev)
-    _grad_norm(arrays, norm, norms, workspace, stream, dev)
-    _grad_clip(arrays, tensors, max_norm, norm, out, factors, stream, dev)
+    st, norm_to = _raw_stream(stream, dev), _norm_outputs(arrays, norm, norms, dev)
+    to, to_kinds, written = _outputs(out, arrays, tensors, dev)
+    limit, factors_to = float(max_norm), _factors(factors, dev)
+    ws, ws_bytes, _keep = _norm_workspace(arrays, workspace, stream, dev)
+    _check(lib().gc_clip_grad_norm(*arrays[3], len(arrays[1]), to.ctypes.data, to_kinds.ctypes.data,
+                                   limit, *norm_to, *factors_to, ws, ws_bytes, st),
+           "gc_clip_grad_norm")
+    _types[4]([*written, norm, *(t for t in (norms, factors) if t is not None)])
 
 
 __all__ = ["Plan", "GCError", "lib", "status_string", "copy_f32", "add_f32", "read_f32", "layout",

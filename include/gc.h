@@ -567,6 +567,8 @@ int gc_gated_linear_backward(const void* dh, int64_t ld_dh, const void* gate, in
  *   max_norm  : >= 0, or Inf.  norm: device float[1], read only.
  *   factors   : device float[n_factors], or NULL: what gc_plan_set_gradient_scale takes, for a gradient
  *               that is flat already (n = 0 then).
+ * gc_clip_grad_norm: gc_grad_norm and gc_grad_clip by its norm, one after the other.  Both calls' arguments
+ * are checked before anything is launched, so that a refused call leaves norm and norms as they were too.
  */
 int gc_grad_norm_workspace(const int64_t* sizes /* host */, int32_t n, int64_t* bytes /* host */);
 int gc_grad_norm(const void* const* tensors /* host */, const int64_t* sizes /* host */,
@@ -576,6 +578,11 @@ int gc_grad_clip(const void* const* tensors /* host */, const int64_t* sizes /* 
                  const int32_t* dtypes /* host */, int32_t n, void* const* out /* host */,
                  const int32_t* out_dtypes /* host */, float max_norm, const float* norm,
                  float* factors, int64_t n_factors, void* stream);
+int gc_clip_grad_norm(const void* const* tensors /* host */, const int64_t* sizes /* host */,
+                      const int32_t* dtypes /* host */, int32_t n, void* const* out /* host */,
+                      const int32_t* out_dtypes /* host */, float max_norm, float* norm, float* norms,
+                      float* factors, int64_t n_factors, void* workspace, int64_t workspace_bytes,
+                      void* stream);
 
 /* Forget the threshold estimates (of Top-k calls and the capture floor of threshold calls):
  * the next call runs as on a fresh plan. */
