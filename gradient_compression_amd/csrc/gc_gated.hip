@@ -45,7 +45,9 @@ __device__ __forceinline__ float exp_neg(float x, float low = 0.0f) {
   return fmaf(e * kLn2, rest, e) * (small ? 0x1p-64f : 1.0f);
 }
 
-// act(g) and its derivative, each within 16 * 2^-24 of its terms.  p is the factor that both start from
+// act(g) and its derivative, each within 16 * 2^-24 of its terms, gelu_tanh within (16 + 5 |v|) * 2^-24: its
+// v is rounded five times before the exponential, which makes an error of |v| of them (as in any fp32 form that
+// does not carry v's low part along; 94 * 2^-24 at g = -6.7).  p is the factor that both start from
 // (the logistic or the normal distribution function) and q what is left to 1, each formed without
 // cancellation.  Arguments are limited to where p is 0 or 1 in fp32 anyway; NaN comes back through g.
 // These take about 25 instructions where the library's exponential, error function and division took 65

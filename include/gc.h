@@ -498,6 +498,9 @@ int gc_act_weight_grad(const void* dy, int64_t ld_dy, int32_t dtype, int64_t row
  *   gate = round(G);  up = round(U)  (what the backward pass starts from; either may be NULL)
  * with act(g) = g / (1 + exp(-g)) (GC_ACT_SILU), g * Phi(g) with the normal distribution function Phi
  * (GC_ACT_GELU), or g / (1 + exp(-2 sqrt(2 / pi) (g + 0.044715 g^3))) (GC_ACT_GELU_TANH), in fp32.
+ * Before the rounding act is within 16 * 2^-24 of its value (silu of |g| <= 16 here within 20), and act' within
+ * as much of its terms; GC_ACT_GELU_TANH within (16 + 5 |v|) * 2^-24 with v = 2 sqrt(2 / pi) (g + 0.044715 g^3),
+ * the exponential's argument, which is rounded before it.
  * Everything shares dtype.  Products of bf16 and fp16 are exact.  An fp32 value is multiplied as the sum
  * of three bf16 values (its 24 bits), the pairs below 2^-23 of a product left out, which its sum rounds
  * away; Inf, NaN and what overflows come out as one fp32 sum has them.  As in gc_act_weight_grad, values
@@ -524,7 +527,7 @@ int gc_gated_linear(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, in
  * The block's backward pass from the kept gate and up:
  *   dgate = round(dh * up * act'(gate));  dup = round(dh * act(gate))  to dtype;
  *   dx = round(dgate w_gate + dup w_up) of dgate and dup as they are stored (fp32 sums, as above),
- * with act' the derivative of act, each within a few units of fp32 of its terms.
+ * with act' the derivative of act.
  *   dgate, dup : may each be dh, gate or up itself (not both the same).
  *   dx         : may be NULL; then only dgate and dup are formed, and cols, the weights and the
  *                workspace are not looked at.
