@@ -14,9 +14,9 @@
 //
 // Measured, 8192 rows, 4096 x 11008 bf16: forward with gate and up kept 1.19 to 1.24 ms (1190 to 1240 TFLOP/s),
 // backward 1.28 to 1.33 ms in all (the stream 0.155, 5.8 TB/s; the product 1.15).  Library products of the
-// same sizes, without the activation and its matrices, take 1.22 and 1.09 ms.  The matrix cores are busy for 70
-// and 77 % of the cycles, LDS (hardly a bank conflict) for 47 and 48 %, at a clock of 1.7 GHz; the forward pass
-// has its results (541 MB) and activations besides, for which its tiles stand still.
+// same sizes, without the activation and its matrices, take 1.11 to 1.22 and 1.06 to 1.09 ms.  The matrix cores
+// are busy for 70 and 77 % of the cycles, LDS (hardly a bank conflict) for 47 and 48 %, at a clock of 1.7 GHz;
+// the forward pass has its results (541 MB) and activations besides, for which its tiles stand still.
 // Loading into LDS directly, 16-byte aligned rows only, was tried first: forward 1.32 ms, backward 1.50.
 #include <type_traits>
 
@@ -714,7 +714,7 @@ __global__ __launch_bounds__(256) void k_product_join(Product g) {
 // A workgroup forms 16 columns of each projection, which are the 32 rows of one operand; its 8 waves share
 // the sum, 128 bytes of the rows at a time, each operand straight from memory, and join their parts in
 // LDS: many workgroups, no second launch.  One row through 4096 x 1024 bf16 takes 4.3 us of the GPU (tiles
-// 8.6), through 11008 x 4096 31 (5.8 TB/s; 32.5).
+// 8.6), through 11008 x 4096 31 (5.8 TB/s; 32.5), both with the weights in the 256 MB cache.
 constexpr int kFewRows = 32, kFewWaves = 8, kFewColumns = 16;
 
 template <int DT, int ACT>
@@ -820,7 +820,8 @@ struct Shape {
 //
 // Where one tile holds all rows nothing shares the weights' loads, which come from memory then: a tiny
 // tile's 16-bit step takes 0.5, 1.0 and 1.6 us, a small one's 0.75 and 1.3 (27 rows through 11008 x 4096 bf16,
-// the weights not in any cache: whole sums 44.7 us, in 4 parts 41.5).
+// the weights not in any cache: whole sums 44.7 us, in 4 parts 41.5; the rule, to which the whole sums are 64
+// steps of 0.5 and 4 us, takes them).  These steps go by the rows alone, whatever the weights' size.
 //
 // Up to 32 rows of a forward pass may go without tiles: 3.5 us, and for each 1 KB of a row's sum 1.65 us (fp32
 // 1.85, ragged 16-bit rows 2.9; less on part of the CUs) and a little more with the rows, with the

@@ -7,10 +7,10 @@
 // large one; it has 4 accesses of 16 bytes a lane in flight (8 gained nothing).
 //
 // Measured: 1.07e9 bf16 elements into one fp32 tensor 1605 us in all, of which the norm reads at 5.9 TB/s and the
-// scaling moves 5.2 TB/s (a plain copy 4.8); 335 M elements in 391 tensors 540 us; 335 M in place under
-// the limit, which nothing is written for, 238 us (5.65 TB/s).  161 tensors of 25 M elements take the GPU
-// 28 us, and the host 66 to 70 us to look at.  Going through the tensors from their end when scaling, where the
-// cache still holds the last ones, gained 1 % at most.
+// scaling moves 5.2 TB/s (a plain read reaches 7.1, a plain copy 5.4); 335 M elements in 391 tensors 540 us;
+// 335 M in place under the limit, which nothing is written for, 238 us (5.65 TB/s), and scaled 789 us.  161
+// tensors of 25 M elements take the GPU 28 us, and the host 60 to 64 us to look at.  Going through the tensors
+// from their end when scaling, where the cache still holds the last ones, gained 1 % at most.
 #include <type_traits>
 
 #include "gc_grads.h"
